@@ -30,6 +30,9 @@ __all__ = [
     "ASSIGN_SCORE", "ASSIGN_VOTE",
     "DEVERR_SINK_LABEL", "DEVERR_LABEL_RANGE", "DEVERR_TAIL_FULL", "DEVERR_TOKEN_CAP", "DEVERR_INDEX",
     "NEIGHBOURS",
+    "Q8_INT8", "Q8_E4M3", "DEVERR_PLAN", "DEVERR_BLOCK", "TableDesc", "Q8Desc", "PlanDesc", "BlockTable", "Q8Cache",
+    "Plan", "block_table", "q8_cache", "new_q8_cache", "new_plan", "q8_shape", "ckv_plan_blocks", "ckv_quant_append",
+    "ckv_q8_read", "ckv_q8_workspace_size", "ckv_dense_decode_q8", "ckv_sparse_decode_q8",
 ]
 
 # the in-tree build, always: no environment variable selects another library
@@ -43,6 +46,8 @@ PER_GROUP, PER_HEAD = 0, 1
 ASSIGN_SCORE, ASSIGN_VOTE = 0, 1
 DEVERR_SINK_LABEL, DEVERR_LABEL_RANGE, DEVERR_TAIL_FULL, DEVERR_TOKEN_CAP, DEVERR_INDEX = 1, 2, 4, 8, 16
 DEVERR_EDGE_CAP = 32
+DEVERR_PLAN, DEVERR_BLOCK = 64, 128
+Q8_INT8, Q8_E4M3 = 0, 1
 NEIGHBOURS = 8
 KERNEL_KINDS = ("build", "score", "select", "attention", "merge", "update", "edges")
 EXPORTED = ("ckv_workspace_size", "ckv_build_centroids", "ckv_score_select", "ckv_sparse_decode",
@@ -50,6 +55,8 @@ EXPORTED = ("ckv_workspace_size", "ckv_build_centroids", "ckv_score_select", "ck
             "ckv_get_device_error", "ckv_kernel_timing", "ckv_kernel_times",
             "ckv_dense_decode",
             "ckv_edges_workspace_size", "ckv_build_edges",
+            "ckv_plan_blocks", "ckv_quant_append", "ckv_q8_read", "ckv_q8_workspace_size", "ckv_dense_decode_q8",
+            "ckv_sparse_decode_q8",
             "ckv_status_string", "ckv_last_error", "ckv_abi_version", "ckv_debug_build")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -85,6 +92,20 @@ class SelectionDesc(ctypes.Structure):
                 ("tok_prefix", _p), ("tail_sel", _p), ("unit_prefix", _p)]
 
 
+class TableDesc(ctypes.Structure):
+    _fields_ = [("B", _i32), ("block", _i32), ("n_blocks", _i32), ("max_blocks", _i32), ("table", _p), ("len", _p),
+                ("free_list", _p), ("n_free", _p), ("dev_err", _p)]
+
+
+class Q8Desc(ctypes.Structure):
+    _fields_ = [("blocks", TableDesc), ("format", _i32), ("dtype", _i32), ("Hkv", _i32), ("Hq", _i32), ("d", _i32),
+                ("k", _p), ("v", _p), ("k_scale", _p), ("v_scale", _p)]
+
+
+class PlanDesc(ctypes.Structure):
+    _fields_ = [("n_rows", _i32), ("start", _p), ("slot", _p), ("granted", _p)]
+
+
 _P = ctypes.POINTER
 
 
@@ -103,13 +124,21 @@ def _declare(lib_: ctypes.CDLL) -> ctypes.CDLL:
     lib_.ckv_edges_workspace_size.argtypes = [_P(CacheDesc), _i32, _i32, _i32, _P(_sz)]
     lib_.ckv_build_edges.argtypes = [_P(CacheDesc), _i32, _i32, _p, _i32, _p, _p, _p, _p, _p, _p, _i32, _p, _p, _sz,
                                      _p]
+    lib_.ckv_plan_blocks.argtypes = [_P(TableDesc), _p, _P(PlanDesc), _p]
+    lib_.ckv_quant_append.argtypes = [_P(Q8Desc), _P(PlanDesc), _p, _p, _i32, _i64, _i64, _i64, _p]
+    lib_.ckv_q8_read.argtypes = [_P(Q8Desc), _p, _i32, _p, _p, _i64, _i64, _i64, _p]
+    lib_.ckv_q8_workspace_size.argtypes = [_P(Q8Desc), _P(GraphDesc), _P(SelectionDesc), _P(_sz)]
+    lib_.ckv_dense_decode_q8.argtypes = [_P(Q8Desc), _p, _p, _p, _sz, _p]
+    lib_.ckv_sparse_decode_q8.argtypes = [_P(Q8Desc), _p, _P(GraphDesc), _P(SelectionDesc), _p, _p, _p, _p, _p, _sz,
+                                          _p]
     lib_.ckv_get_device_error.argtypes = [_P(GraphDesc), _p, _P(ctypes.c_int32), _i32]
     lib_.ckv_kernel_timing.argtypes = [_i32]
     lib_.ckv_kernel_times.argtypes = [_P(ctypes.c_float), _P(ctypes.c_int32), _i32]
     for f in ("ckv_workspace_size", "ckv_build_centroids", "ckv_score_select", "ckv_sparse_decode",
               "ckv_sparse_decode_noalloc", "ckv_assign_update", "ckv_append_assign", "ckv_sparse_decode_append",
               "ckv_dense_decode", "ckv_get_device_error", "ckv_kernel_timing", "ckv_kernel_times",
-              "ckv_edges_workspace_size", "ckv_build_edges"):
+              "ckv_edges_workspace_size", "ckv_build_edges", "ckv_plan_blocks", "ckv_quant_append", "ckv_q8_read",
+              "ckv_q8_workspace_size", "ckv_dense_decode_q8", "ckv_sparse_decode_q8"):
         getattr(lib_, f).restype = ctypes.c_int
     lib_.ckv_status_string.argtypes = [ctypes.c_int]
     lib_.ckv_status_string.restype = ctypes.c_char_p
@@ -357,11 +386,13 @@ def ckv_kernel_times() -> dict:
     return {k: (float(ms[i]), int(cnt[i])) for i, k in enumerate(KERNEL_KINDS)}
 
 
-def ckv_get_device_error(graph: Graph, reset: bool = False, stream=None) -> int:
-    """The graph's device error word (OR of DEVERR_* bits) once the stream's
-    queued work is done; reset=True zeroes it afterwards."""
+def ckv_get_device_error(graph, reset: bool = False, stream=None) -> int:
+    """The device error word (OR of DEVERR_* bits) of a Graph, a BlockTable or
+    a Q8Cache once the stream's queued work is done; reset=True zeroes it
+    afterwards."""
     code = ctypes.c_int32(0)
-    _check(lib.ckv_get_device_error(ctypes.byref(graph.desc), _stream(stream), ctypes.byref(code), int(reset)),
+    desc = graph.desc if isinstance(graph.desc, GraphDesc) else GraphDesc(dev_err=graph.dev_err.data_ptr())
+    _check(lib.ckv_get_device_error(ctypes.byref(desc), _stream(stream), ctypes.byref(code), int(reset)),
            "ckv_get_device_error")
     return int(code.value)
 
@@ -443,3 +474,259 @@ def ckv_build_edges(cache: CacheDesc, mode: int, S: int, q_prefill: torch.Tensor
                                edges.co_w.data_ptr(), edges.co_n.data_ptr(), edges.co_src.shape[1],
                                edges.dev_err.data_ptr(), edges.ws.data_ptr(), edges.ws.numel(), _stream(stream)),
            "ckv_build_edges")
+
+
+# ----------------------------------------------------------------------------
+# the paged 8-bit cache
+# ----------------------------------------------------------------------------
+
+_Q8_CODES = {torch.int8: Q8_INT8, torch.float8_e4m3fn: Q8_E4M3}
+_Q8_FORMATS = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+_ROW_TYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
+def _need(name: str, t: torch.Tensor, dtype, shape, device) -> int:
+    """The data pointer of a tensor that has to be contiguous, of this dtype
+    and shape, on this device."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} (strides {t.stride()}) on {t.device}")
+    return t.data_ptr()
+
+
+def _call(where: str, fn, device: torch.device, stream, *args) -> None:
+    """Runs an entry point on the tensors' device: on its current stream unless
+    one is given, with that device current."""
+    if device.type != "cuda":
+        raise ValueError(f"{where}: tensors must be on a CUDA device, not {device}")
+    if stream is None:
+        raw = torch.cuda.current_stream(device).cuda_stream
+    else:
+        raw = _stream(stream)
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, raw)
+    if status != 0:
+        _check(status, where)
+
+
+@dataclass
+class BlockTable:
+    """The blocks of a batch of requests and those that are free (ckv_table_desc)."""
+    desc: TableDesc
+    table: torch.Tensor      # int32 [B, max_blocks]
+    len: torch.Tensor        # int32 [B]
+    free_list: Optional[torch.Tensor]  # int32 [n_blocks]
+    n_free: Optional[torch.Tensor]     # int32 [1]
+    dev_err: torch.Tensor    # int32 [1]
+
+
+@dataclass
+class Q8Cache:
+    """A paged 8-bit cache (ckv_q8_desc); `dtype` is that of q and of the rows."""
+    desc: Q8Desc
+    blocks: BlockTable
+    k: torch.Tensor          # int8 or float8_e4m3fn [n_blocks, Hkv, block, d]
+    v: torch.Tensor
+    k_scale: torch.Tensor    # fp32 [n_blocks, Hkv]
+    v_scale: torch.Tensor
+    dtype: torch.dtype
+
+    @property
+    def dev_err(self) -> torch.Tensor:
+        return self.blocks.dev_err
+
+    @property
+    def table(self) -> torch.Tensor:
+        return self.blocks.table
+
+    @property
+    def len(self) -> torch.Tensor:
+        return self.blocks.len
+
+
+@dataclass
+class Plan:
+    """Where a batch of new tokens goes (ckv_plan_desc)."""
+    start: torch.Tensor      # int32 [B + 1]
+    slot: torch.Tensor       # int32 [n_rows]
+    granted: torch.Tensor    # int32 [B]
+
+    def __post_init__(self):
+        B, dev = self.granted.shape[0], self.granted.device
+        self.desc = PlanDesc(self.slot.numel(), _need("start", self.start, torch.int32, (B + 1,), dev),
+                             _need("slot", self.slot, torch.int32, (self.slot.numel(),), dev),
+                             _need("granted", self.granted, torch.int32, (B,), dev))
+
+
+def block_table(table: torch.Tensor, length: torch.Tensor, free_list: Optional[torch.Tensor],
+                n_free: Optional[torch.Tensor], block: int, dev_err: Optional[torch.Tensor] = None,
+                n_blocks: Optional[int] = None) -> BlockTable:
+    """Describe existing tensors; n_blocks defaults to the free list's length."""
+    if table.dim() != 2:
+        raise ValueError("table must be int32 [B, max_blocks]")
+    B, width = table.shape
+    dev = table.device
+    if dev_err is None:
+        dev_err = torch.zeros((1,), dtype=torch.int32, device=dev)
+    if n_blocks is None:
+        if free_list is None:
+            raise ValueError("n_blocks is needed without a free list")
+        n_blocks = free_list.shape[0]
+    desc = TableDesc(B, block, n_blocks, width, _need("table", table, torch.int32, (B, width), dev),
+                     _need("length", length, torch.int32, (B,), dev),
+                     None if free_list is None else _need("free_list", free_list, torch.int32, (n_blocks,), dev),
+                     None if n_free is None else _need("n_free", n_free, torch.int32, (1,), dev),
+                     _need("dev_err", dev_err, torch.int32, (1,), dev))
+    return BlockTable(desc, table, length, free_list, n_free, dev_err)
+
+
+def q8_cache(k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, table: torch.Tensor,
+             length: torch.Tensor, Hq: int, dtype: torch.dtype = torch.bfloat16,
+             free_list: Optional[torch.Tensor] = None, n_free: Optional[torch.Tensor] = None,
+             dev_err: Optional[torch.Tensor] = None) -> Q8Cache:
+    """Describe an existing pool [n_blocks, Hkv, block, d] of int8 or
+    float8_e4m3fn codes with its scales, table and lengths."""
+    if k.dim() != 4 or k.dtype not in _Q8_CODES:
+        raise ValueError("k must be int8 or float8_e4m3fn [n_blocks, Hkv, block, d]")
+    if dtype not in _ROW_TYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    n_blocks, Hkv, block, d = k.shape
+    dev = k.device
+    bt = block_table(table, length, free_list, n_free, block, dev_err, n_blocks)
+    if table.device != dev:
+        raise ValueError("the table must be on the pool's device")
+    desc = Q8Desc(bt.desc, _Q8_CODES[k.dtype], _ROW_TYPES[dtype], Hkv, Hq, d, _need("k", k, k.dtype, k.shape, dev),
+                  _need("v", v, k.dtype, k.shape, dev), _need("k_scale", k_scale, torch.float32, (n_blocks, Hkv), dev),
+                  _need("v_scale", v_scale, torch.float32, (n_blocks, Hkv), dev))
+    return Q8Cache(desc, bt, k, v, k_scale, v_scale, dtype)
+
+
+def new_q8_cache(B: int, Hkv: int, Hq: int, d: int, n_blocks: int, block: int = 64, max_blocks: Optional[int] = None,
+                 fmt: str = "int8", dtype: torch.dtype = torch.bfloat16, device="cuda") -> Q8Cache:
+    """An empty pool: B requests of length 0, every block free (block 0 is
+    taken first).  fmt: "int8" or "e4m3"."""
+    if fmt not in _Q8_FORMATS:
+        raise ValueError(f"unknown format {fmt!r}")
+    i32 = dict(dtype=torch.int32, device=device)
+    k = torch.zeros((n_blocks, Hkv, block, d), dtype=torch.uint8, device=device).view(_Q8_FORMATS[fmt])
+    scale = torch.ones((n_blocks, Hkv), dtype=torch.float32, device=device)
+    return q8_cache(k, torch.zeros_like(k.view(torch.uint8)).view(k.dtype), scale, scale.clone(),
+                    torch.full((B, n_blocks if max_blocks is None else max_blocks), -1, **i32),
+                    torch.zeros((B,), **i32), Hq, dtype,
+                    torch.arange(n_blocks - 1, -1, -1, **i32), torch.full((1,), n_blocks, **i32))
+
+
+def new_plan(cache, n_rows: int) -> Plan:
+    """Buffers for ckv_plan_blocks on a BlockTable or Q8Cache; n_rows bounds
+    the tokens that the batch may add."""
+    length = cache.len
+    i32 = dict(dtype=torch.int32, device=length.device)
+    B = length.shape[0]
+    return Plan(torch.zeros((B + 1,), **i32), torch.full((n_rows,), -1, **i32), torch.zeros((B,), **i32))
+
+
+def q8_shape(cache: Q8Cache, T_cap: int) -> CacheDesc:
+    """The cache's shapes, for new_graph, new_selection and ckv_score_select."""
+    c = cache.desc
+    return CacheDesc(c.dtype, c.blocks.B, c.Hkv, c.Hq, c.d, T_cap, None, None, 0, 0, 0)
+
+
+def _of_plan(cache, plan: Plan) -> None:
+    if plan.granted.shape[0] != cache.len.shape[0] or plan.granted.device != cache.len.device:
+        raise ValueError("the plan was made for another batch size or device")
+
+
+def ckv_plan_blocks(cache, add: torch.Tensor, plan: Plan, stream=None) -> None:
+    """Request b of a BlockTable or Q8Cache changes by add[b] tokens (int32 [B])."""
+    bt = cache.blocks if isinstance(cache, Q8Cache) else cache
+    _of_plan(bt, plan)
+    dev = bt.len.device
+    _call("ckv_plan_blocks", lib.ckv_plan_blocks, dev, stream, ctypes.byref(bt.desc),
+          _need("add", add, torch.int32, bt.len.shape, dev), ctypes.byref(plan.desc))
+
+
+def ckv_quant_append(cache: Q8Cache, plan: Plan, k_new: torch.Tensor, v_new: torch.Tensor, stream=None) -> None:
+    """k_new, v_new: packed rows [n_rows, Hkv, d], or padded ones [B, T, Hkv, d]
+    of which request b's first granted[b] count; cache dtype, any strides with
+    contiguous rows of 16-byte multiples, the same for both."""
+    _of_plan(cache, plan)
+    c, dev = cache.desc, cache.k.device
+    n = plan.slot.numel()
+    if k_new.dim() == 3:
+        shape, T_rows = (n, c.Hkv, c.d), 0
+    elif k_new.dim() == 4:
+        T_rows = k_new.shape[1]
+        shape = (c.blocks.B, T_rows, c.Hkv, c.d)
+    else:
+        raise ValueError("k_new must be [n_rows, Hkv, d] or [B, T, Hkv, d]")
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if t.shape != shape or t.dtype != cache.dtype or t.device != dev or t.stride() != k_new.stride() or t.stride(-1) != 1:
+            raise ValueError(f"{name} must be a {cache.dtype} tensor of shape {shape} on {dev} with contiguous rows and "
+                             f"k_new's strides, got {t.dtype} {tuple(t.shape)} {t.stride()} on {t.device}")
+    if n == 0 or k_new.numel() == 0:
+        return
+    sb, st, sh = (0, k_new.stride(0), k_new.stride(1)) if T_rows == 0 else k_new.stride()[:3]
+    _call("ckv_quant_append", lib.ckv_quant_append, dev, stream, ctypes.byref(c), ctypes.byref(plan.desc),
+          k_new.data_ptr(), v_new.data_ptr(), T_rows, sb, st, sh)
+
+
+def ckv_q8_read(cache: Q8Cache, k_out: torch.Tensor, v_out: torch.Tensor, first: Optional[torch.Tensor] = None,
+                stream=None) -> None:
+    """Fills k_out and v_out, [B, Hkv, R, d] in the cache dtype, with positions
+    first[b] .. first[b] + R - 1 (first None: from 0); zeros past a request's
+    end."""
+    c, dev = cache.desc, cache.k.device
+    if k_out.dim() != 4:
+        raise ValueError("k_out must be [B, Hkv, R, d]")
+    R = k_out.shape[2]
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if (t.shape != (c.blocks.B, c.Hkv, R, c.d) or t.dtype != cache.dtype or t.device != dev
+                or t.stride() != k_out.stride() or t.stride(-1) != 1):
+            raise ValueError(f"{name} must be a {cache.dtype} [B, Hkv, R, d] tensor on {dev} with contiguous rows and "
+                             f"k_out's strides, got {t.dtype} {tuple(t.shape)} {t.stride()} on {t.device}")
+    at = None if first is None else _need("first", first, torch.int32, cache.len.shape, dev)
+    _call("ckv_q8_read", lib.ckv_q8_read, dev, stream, ctypes.byref(c), at, R, k_out.data_ptr(), v_out.data_ptr(),
+          k_out.stride(0), k_out.stride(1), k_out.stride(2))
+
+
+def ckv_q8_workspace_size(cache: Q8Cache, graph: Optional[Graph] = None, sel: Optional[Selection] = None) -> int:
+    out = _sz(0)
+    g = ctypes.byref(graph.desc) if graph is not None else None
+    s = ctypes.byref(sel.desc) if sel is not None else None
+    _check(lib.ckv_q8_workspace_size(ctypes.byref(cache.desc), g, s, ctypes.byref(out)), "ckv_q8_workspace_size")
+    return int(out.value)
+
+
+def _q8_attention(cache: Q8Cache, q: torch.Tensor, out: torch.Tensor, ws: torch.Tensor):
+    c, dev = cache.desc, cache.k.device
+    shape = (c.blocks.B, c.Hq, c.d)
+    if ws.device != dev:
+        raise ValueError("the workspace is on another device")
+    return dev, _need("q", q, cache.dtype, shape, dev), _need("out", out, torch.float32, shape, dev)
+
+
+def ckv_dense_decode_q8(cache: Q8Cache, q: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """out [B, Hq, d] fp32: attention of q [B, Hq, d] over each request's tokens."""
+    dev, qp, op = _q8_attention(cache, q, out, ws)
+    _call("ckv_dense_decode_q8", lib.ckv_dense_decode_q8, dev, stream, ctypes.byref(cache.desc), qp, op, ws.data_ptr(),
+          ws.numel())
+
+
+def ckv_sparse_decode_q8(cache: Q8Cache, q: torch.Tensor, graph: Graph, sel: Selection, out: torch.Tensor,
+                         nbr8: Optional[torch.Tensor], ws: torch.Tensor, k_new: Optional[torch.Tensor] = None,
+                         assigned: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Attention over the selected positions; with k_new [B, Hkv, d] the new
+    token also joins a community (ckv_sparse_decode_append without the rows)."""
+    dev, qp, op = _q8_attention(cache, q, out, ws)
+    c = cache.desc
+    if graph.dev_err.device != dev or sel.sel_tok.device != dev:
+        raise ValueError("the graph and the selection must be on the cache's device")
+    kp = None if k_new is None else _need("k_new", k_new, cache.dtype, (c.blocks.B, c.Hkv, c.d), dev)
+    U = graph.U
+    np_ = None if nbr8 is None else _need("nbr8", nbr8, torch.int32, (U, NEIGHBOURS), dev)
+    ap = None if assigned is None else _need("assigned", assigned, torch.int32, (U,), dev)
+    _call("ckv_sparse_decode_q8", lib.ckv_sparse_decode_q8, dev, stream, ctypes.byref(c), qp, ctypes.byref(graph.desc),
+          ctypes.byref(sel.desc), op, np_, kp, ap, ws.data_ptr(), ws.numel())

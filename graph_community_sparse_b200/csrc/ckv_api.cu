@@ -8,6 +8,7 @@
 
 #include "ckv_assign.cuh"
 #include "ckv_internal.cuh"
+#include "ckv_q8.cuh"
 
 namespace {
 
@@ -159,6 +160,124 @@ ckv::SelView sel_view(const ckv_selection_desc* s) {
     v.tok_prefix = s->tok_prefix;
     v.tail_sel = s->tail_sel;
     return v;
+}
+
+// The paged 8-bit cache.  `pool`: the call takes and gives back blocks.
+ckv_status check_table(const ckv_table_desc* t, bool pool) {
+    if (!t) return fail(CKV_ERR_INVALID_ARG, "block table descriptor is NULL");
+    if (t->B < 1 || t->n_blocks < 1 || t->max_blocks < 1)
+        return fail(CKV_ERR_INVALID_ARG, "B, n_blocks and max_blocks must be >= 1");
+    if (t->block != 16 && t->block != 32 && t->block != 64 && t->block != 128)
+        return fail(CKV_ERR_UNSUPPORTED, "block = %d not in {16,32,64,128}", t->block);
+    if (t->B > ckv::MAX_UNITS) return fail(CKV_ERR_UNSUPPORTED, "B = %d above %d", t->B, ckv::MAX_UNITS);
+    if ((int64_t)t->n_blocks * t->block > 0x7fffffffll || (int64_t)t->max_blocks * t->block > 0x7fffffffll)
+        return fail(CKV_ERR_UNSUPPORTED, "n_blocks * block or max_blocks * block above 2^31 - 1");
+    if (!t->table || !t->len || !t->dev_err) return fail(CKV_ERR_INVALID_ARG, "table, len or dev_err is NULL");
+    if (pool && (!t->free_list || !t->n_free)) return fail(CKV_ERR_INVALID_ARG, "free_list or n_free is NULL");
+    return CKV_OK;
+}
+
+ckv_status check_plan(const ckv_plan_desc* p) {
+    if (!p) return fail(CKV_ERR_INVALID_ARG, "plan descriptor is NULL");
+    if (p->n_rows < 0) return fail(CKV_ERR_INVALID_ARG, "n_rows < 0");
+    if (!p->start || !p->granted || (p->n_rows > 0 && !p->slot))
+        return fail(CKV_ERR_INVALID_ARG, "start, slot or granted is NULL");
+    return CKV_OK;
+}
+
+ckv_status check_q8(const ckv_q8_desc* c) {
+    if (!c) return fail(CKV_ERR_INVALID_ARG, "8-bit cache descriptor is NULL");
+    const ckv_status s = check_table(&c->blocks, false);
+    if (s != CKV_OK) return s;
+    if (c->format != CKV_Q8_INT8 && c->format != CKV_Q8_E4M3)
+        return fail(CKV_ERR_UNSUPPORTED, "format %d is not CKV_Q8_INT8 or CKV_Q8_E4M3", c->format);
+    if (c->dtype != CKV_DTYPE_F32 && c->dtype != CKV_DTYPE_BF16)
+        return fail(CKV_ERR_UNSUPPORTED, "dtype %d is not CKV_DTYPE_F32 or CKV_DTYPE_BF16", c->dtype);
+    if (c->Hkv < 1 || c->Hq < 1 || c->Hq % c->Hkv != 0)
+        return fail(CKV_ERR_INVALID_ARG, "Hkv and Hq must be >= 1 and Hq %% Hkv == 0");
+    const int gq = c->Hq / c->Hkv;
+    if (gq != 1 && gq != 2 && gq != 4 && gq != 8)
+        return fail(CKV_ERR_UNSUPPORTED, "Hq/Hkv = %d not in {1,2,4,8}", gq);
+    if (c->d != 64 && c->d != 128) return fail(CKV_ERR_UNSUPPORTED, "d = %d not in {64,128}", c->d);
+    if ((int64_t)c->blocks.n_blocks * c->Hkv * c->blocks.block > 0x7fffffffll)
+        return fail(CKV_ERR_UNSUPPORTED, "n_blocks * Hkv * block above 2^31 - 1");
+    if ((int64_t)c->blocks.B * c->Hkv > ckv::MAX_UNITS)
+        return fail(CKV_ERR_UNSUPPORTED, "B * Hkv = %lld above %d", (long long)c->blocks.B * c->Hkv, ckv::MAX_UNITS);
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale) return fail(CKV_ERR_INVALID_ARG, "a pool pointer is NULL");
+    if (!aligned16(c->k) || !aligned16(c->v)) return fail(CKV_ERR_MISALIGNED, "k and v must be 16-byte aligned");
+    return CKV_OK;
+}
+
+// rows in the caller's layout: 16-byte aligned, element strides
+ckv_status check_rows(const ckv_q8_desc* c, const void* k, const void* v, int64_t sb, int64_t st, int64_t sh) {
+    if (!k || !v) return fail(CKV_ERR_INVALID_ARG, "a rows pointer is NULL");
+    const int64_t es = elem_size(c->dtype);
+    if (!aligned16(k) || !aligned16(v) || (sb * es) % 16 || (st * es) % 16 || (sh * es) % 16)
+        return fail(CKV_ERR_MISALIGNED, "rows and their byte strides must be multiples of 16");
+    if (sb < 0 || st < 0 || sh < 0) return fail(CKV_ERR_INVALID_ARG, "strides must not be negative");
+    return CKV_OK;
+}
+
+ckv::TableView table_view(const ckv_table_desc* t) {
+    ckv::TableView v;
+    v.B = t->B;
+    v.block = t->block;
+    v.n_blocks = t->n_blocks;
+    v.max_blocks = t->max_blocks;
+    v.sh = t->block == 16 ? 4 : t->block == 32 ? 5 : t->block == 64 ? 6 : 7;
+    v.table = t->table;
+    v.len = t->len;
+    v.free_list = t->free_list;
+    v.n_free = t->n_free;
+    v.dev_err = t->dev_err;
+    return v;
+}
+
+ckv::Q8View q8_view(const ckv_q8_desc* c) {
+    ckv::Q8View v;
+    v.t = table_view(&c->blocks);
+    v.format = c->format;
+    v.dtype = c->dtype;
+    v.Hkv = c->Hkv;
+    v.Hq = c->Hq;
+    v.d = c->d;
+    v.k = c->k;
+    v.v = c->v;
+    v.k_scale = c->k_scale;
+    v.v_scale = c->v_scale;
+    return v;
+}
+
+// The shapes of an 8-bit cache as the graph checks take them.
+ckv_cache_desc q8_shape(const ckv_q8_desc* c, int T_cap) {
+    ckv_cache_desc s{};
+    s.dtype = c->dtype;
+    s.B = c->blocks.B;
+    s.Hkv = c->Hkv;
+    s.Hq = c->Hq;
+    s.d = c->d;
+    s.T_cap = T_cap;
+    return s;
+}
+
+ckv_status check_q8_graph(const ckv_q8_desc* c, const ckv_graph_desc* g) {
+    if (!g) return fail(CKV_ERR_INVALID_ARG, "graph descriptor is NULL");
+    if ((int64_t)g->T_cap > (int64_t)c->blocks.max_blocks * c->blocks.block)
+        return fail(CKV_ERR_CAPACITY, "graph T_cap = %d above max_blocks * block", g->T_cap);
+    const ckv_cache_desc s = q8_shape(c, g->T_cap);
+    if (s.T_cap < 1) return fail(CKV_ERR_INVALID_ARG, "T_cap must be >= 1");
+    return check_graph(&s, g);
+}
+
+// head, counters, then the larger of the two calls' parts
+size_t q8_ws_bytes(const ckv_q8_desc* c, const ckv_graph_desc* g, int tok_cap) {
+    size_t need = ckv::q8_dense_ws_bytes(c->Hq / c->Hkv, c->d);
+    if (g) {
+        const int G = g->mode == CKV_GRAPH_PER_HEAD ? c->Hq : c->Hkv;
+        const size_t s = ckv::decode_ws_bytes(c->blocks.B * G, c->Hq / G, c->d, tok_cap);
+        need = need > s ? need : s;
+    }
+    return ckv::WS_RESERVED + ckv::q8_counter_bytes(c->blocks.B * c->Hkv) + need;
 }
 
 #define CKV_TRY(expr)                      \
@@ -422,6 +541,82 @@ ckv_status ckv_dense_decode(const ckv_cache_desc* cache, const void* q, int32_t 
     return cuda_status(ckv::launch_dense_decode(cache_view(cache), q, T, out, ws,
                                                 reinterpret_cast<cudaStream_t>(stream)),
                        "ckv_dense_decode");
+}
+
+ckv_status ckv_plan_blocks(const ckv_table_desc* blocks, const int32_t* add, const ckv_plan_desc* plan,
+                           ckv_stream_t stream) {
+    CKV_TRY(check_table(blocks, true));
+    CKV_TRY(check_plan(plan));
+    if (!add) return fail(CKV_ERR_INVALID_ARG, "add is NULL");
+    ckv::PlanView pv{plan->n_rows, plan->start, plan->slot, plan->granted};
+    return cuda_status(ckv::launch_plan_blocks(table_view(blocks), add, pv, reinterpret_cast<cudaStream_t>(stream)),
+                       "ckv_plan_blocks");
+}
+
+ckv_status ckv_quant_append(const ckv_q8_desc* cache, const ckv_plan_desc* plan, const void* k_new, const void* v_new,
+                            int32_t T_rows, int64_t stride_b, int64_t stride_t, int64_t stride_h,
+                            ckv_stream_t stream) {
+    CKV_TRY(check_q8(cache));
+    CKV_TRY(check_plan(plan));
+    if (T_rows < 0) return fail(CKV_ERR_INVALID_ARG, "T_rows < 0");
+    if (plan->n_rows == 0) return ok();  // no row has a slot
+    CKV_TRY(check_rows(cache, k_new, v_new, stride_b, stride_t, stride_h));
+    ckv::PlanView pv{plan->n_rows, plan->start, plan->slot, plan->granted};
+    ckv::RowsView rv{const_cast<void*>(k_new), const_cast<void*>(v_new), stride_b, stride_t, stride_h, T_rows};
+    return cuda_status(ckv::launch_quant_append(q8_view(cache), pv, rv, reinterpret_cast<cudaStream_t>(stream)),
+                       "ckv_quant_append");
+}
+
+ckv_status ckv_q8_read(const ckv_q8_desc* cache, const int32_t* first, int32_t R, void* k_out, void* v_out,
+                       int64_t stride_b, int64_t stride_h, int64_t stride_t, ckv_stream_t stream) {
+    CKV_TRY(check_q8(cache));
+    if (R < 0) return fail(CKV_ERR_INVALID_ARG, "R < 0");
+    if (R == 0) return ok();
+    CKV_TRY(check_rows(cache, k_out, v_out, stride_b, stride_t, stride_h));
+    if (stride_t < cache->d) return fail(CKV_ERR_INVALID_ARG, "stride_t < d: rows would overlap");
+    if ((int64_t)cache->blocks.B * cache->Hkv * (((int64_t)R + 31) / 32) > 0x7fffffffll)
+        return fail(CKV_ERR_UNSUPPORTED, "B * Hkv * R too large");
+    ckv::RowsView rv{k_out, v_out, stride_b, stride_t, stride_h, 0};
+    return cuda_status(ckv::launch_q8_read(q8_view(cache), first, R, rv, reinterpret_cast<cudaStream_t>(stream)),
+                       "ckv_q8_read");
+}
+
+ckv_status ckv_q8_workspace_size(const ckv_q8_desc* cache, const ckv_graph_desc* graph, const ckv_selection_desc* sel,
+                                 size_t* bytes) {
+    if (!bytes) return fail(CKV_ERR_INVALID_ARG, "bytes is NULL");
+    CKV_TRY(check_q8(cache));
+    if (graph) CKV_TRY(check_q8_graph(cache, graph));
+    *bytes = q8_ws_bytes(cache, graph, sel ? sel->tok_cap : graph ? graph->T_cap : 0);
+    return ok();
+}
+
+ckv_status ckv_dense_decode_q8(const ckv_q8_desc* cache, const void* q, float* out, void* ws, size_t ws_bytes,
+                               ckv_stream_t stream) {
+    CKV_TRY(check_q8(cache));
+    if (!q || !out) return fail(CKV_ERR_INVALID_ARG, "q or out is NULL");
+    if (!aligned16(q) || !aligned16(out)) return fail(CKV_ERR_MISALIGNED, "q and out must be 16-byte aligned");
+    if ((int64_t)cache->blocks.B * cache->Hkv * cache->blocks.max_blocks * (cache->blocks.block / 16) > (int64_t)1 << 30)
+        return fail(CKV_ERR_UNSUPPORTED, "B * Hkv * max_blocks * block above 2^34");
+    CKV_TRY(check_ws(ws, ws_bytes, q8_ws_bytes(cache, nullptr, 0)));
+    return cuda_status(ckv::launch_dense_decode_q8(q8_view(cache), q, out, ws, reinterpret_cast<cudaStream_t>(stream)),
+                       "ckv_dense_decode_q8");
+}
+
+ckv_status ckv_sparse_decode_q8(const ckv_q8_desc* cache, const void* q, const ckv_graph_desc* graph,
+                                const ckv_selection_desc* sel, float* out, int32_t* nbr8, const void* k_new,
+                                int32_t* assigned, void* ws, size_t ws_bytes, ckv_stream_t stream) {
+    CKV_TRY(check_q8(cache));
+    CKV_TRY(check_q8_graph(cache, graph));
+    const ckv_cache_desc shape = q8_shape(cache, graph->T_cap);
+    const int64_t U = (int64_t)cache->blocks.B * graphs_per_seq(&shape, graph);
+    CKV_TRY(check_sel(graph, sel, U));
+    if (!q || !out) return fail(CKV_ERR_INVALID_ARG, "q or out is NULL");
+    if (!aligned16(q) || !aligned16(out)) return fail(CKV_ERR_MISALIGNED, "q and out must be 16-byte aligned");
+    if (k_new && !aligned16(k_new)) return fail(CKV_ERR_MISALIGNED, "k_new must be 16-byte aligned");
+    CKV_TRY(check_ws(ws, ws_bytes, q8_ws_bytes(cache, graph, sel->tok_cap)));
+    return cuda_status(ckv::launch_sparse_decode_q8(q8_view(cache), graph_view(&shape, graph), sel_view(sel), q, out,
+                                                    nbr8, k_new, assigned, ws, reinterpret_cast<cudaStream_t>(stream)),
+                       "ckv_sparse_decode_q8");
 }
 
 }  // extern "C"

@@ -65,7 +65,7 @@ extern "C" {
 #define CKV_API
 #endif
 
-#define CKV_ABI_VERSION 7
+#define CKV_ABI_VERSION 8
 #define CKV_NEIGHBOURS 8
 
 typedef struct CUstream_st* ckv_stream_t; /* the same handle as cudaStream_t */
@@ -102,6 +102,9 @@ typedef enum { CKV_ASSIGN_SCORE = 0, CKV_ASSIGN_VOTE = 1 } ckv_assign_rule;
 #define CKV_DEVERR_TAIL_FULL 4    /* ckv_assign_update found the tail full; not joined */
 #define CKV_DEVERR_TOKEN_CAP 8    /* a selection longer than tok_cap was truncated     */
 #define CKV_DEVERR_EDGE_CAP 32    /* ckv_build_edges: more co-attention pairs than pair_cap */
+#define CKV_DEVERR_PLAN 64        /* ckv_plan_blocks refused a request's growth (granted = 0)          */
+#define CKV_DEVERR_BLOCK 128      /* 8-bit cache: a length, a slot or a block id of the table was
+                                     out of range (checked in every build); its tokens were skipped   */
 #define CKV_DEVERR_INDEX 16       /* debug builds: an index read from a caller's array
                                      (a position, a run offset, a token count, a tail
                                      length) was out of range; the access was skipped */
@@ -376,10 +379,182 @@ CKV_API ckv_status ckv_build_edges(const ckv_cache_desc* cache, int32_t mode, in
                                    size_t ws_bytes, ckv_stream_t stream);
 
 /*
+ * ------------------------------------------------------------------------
+ * The paged 8-bit cache.
+ *
+ * The whole cache stays, as everywhere in this library; here it is kept in 8
+ * bits (half the bytes that the decode attention reads), in blocks that a
+ * batch of requests of different lengths share.
+ *   pool     n_blocks blocks of `block` tokens; block x holds for every KV head
+ *            h the rows k[x, h, 0..block) and v[x, h, 0..block) of d codes and
+ *            one scale each, k_scale[x, h] and v_scale[x, h]: the value held is
+ *            code * scale (fp32).
+ *   table    int32 [B, max_blocks]: the blocks of request b in order; position t
+ *            of request b is row t % block of block table[b, t / block], its
+ *            slot is block id * block + row.  Entries past the request's last
+ *            block are -1.
+ *   len      int32 [B]: positions [0, len[b]) are filled.
+ *   free_list int32 [n_blocks], n_free int32 [1]: entries [0, n_free) are the
+ *            blocks that no request holds, a stack with its top at n_free - 1.
+ *            Only ckv_plan_blocks uses them; NULL for the other calls.
+ *   dev_err  int32 [1] as in ckv_graph_desc.
+ * Every length, slot and block id that a kernel uses is checked on the device
+ * in every build: a bad one sets CKV_DEVERR_BLOCK and the tokens that it names
+ * are skipped (attention, append) or read as zeros (ckv_q8_read).
+ * block is 16, 32, 64 or 128; max_blocks >= 1; 1 <= B <= 8192;
+ * n_blocks * Hkv * block < 2^31.
+ */
+typedef enum { CKV_Q8_INT8 = 0, CKV_Q8_E4M3 = 1 } ckv_q8_format;
+
+typedef struct {
+    int32_t B;
+    int32_t block;
+    int32_t n_blocks;
+    int32_t max_blocks;
+    int32_t* table;
+    int32_t* len;
+    int32_t* free_list;
+    int32_t* n_free;
+    int32_t* dev_err;
+} ckv_table_desc;
+
+/*
+ * k, v: codes [n_blocks, Hkv, block, d], contiguous, 16-byte aligned.
+ * k_scale, v_scale: fp32 [n_blocks, Hkv].  dtype: that of q and of the rows
+ * appended and read back.
+ */
+typedef struct {
+    ckv_table_desc blocks;
+    int32_t format; /* ckv_q8_format */
+    int32_t dtype;  /* ckv_dtype */
+    int32_t Hkv;
+    int32_t Hq;
+    int32_t d;
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+} ckv_q8_desc;
+
+/*
+ * What ckv_plan_blocks decided for one batch of new tokens.  The new tokens'
+ * rows are laid end to end in request order, those of refused requests too.
+ *   start    int32 [B+1]  request b's rows are [start[b], start[b+1])
+ *   slot     int32 [n_rows] the slot of each row; -1 for rows of a refused
+ *            request and for rows past start[B].  NULL when n_rows = 0.
+ *   granted  int32 [B]    the change of len[b]: tokens added, or minus the
+ *            tokens dropped
+ */
+typedef struct {
+    int32_t n_rows;
+    int32_t* start;
+    int32_t* slot;
+    int32_t* granted;
+} ckv_plan_desc;
+
+/*
+ * Block tables and the slot map from request lengths, on the GPU: request b
+ * changes by add[b] tokens (int32 [B]).
+ *   add[b] < 0   drops min(-add[b], len[b]) tokens from the end (rejected
+ *                draft tokens; -len[b] ends the request).  Blocks left
+ *                without a token go back to the free list.
+ *   add[b] > 0   appends; blocks are taken from the free list (those given
+ *                back by the same call included) when the last one is full.
+ * Growth is refused (granted[b] = 0, nothing of the request changes,
+ * CKV_DEVERR_PLAN) when it would pass max_blocks, when its rows would pass
+ * n_rows, or when the blocks needed by the requests up to and including b
+ * (refusals for the first two reasons aside) exceed the free ones; a request
+ * that needs no new block is never refused for want of blocks.  A request
+ * whose len[b] is negative or beyond max_blocks * block is left as it is
+ * (CKV_DEVERR_BLOCK).
+ * Order, so that results are reproducible: the k-th block needed (by request,
+ * then position) is free_list[n_free - 1 - k], and a drop puts its blocks back
+ * so that a growth of the same requests takes the same blocks again.  Entries
+ * of free_list past the new n_free keep what they held.
+ * table, len, free_list and n_free are updated in place.  One launch.
+ */
+CKV_API ckv_status ckv_plan_blocks(const ckv_table_desc* blocks, const int32_t* add, const ckv_plan_desc* plan,
+                                   ckv_stream_t stream);
+
+/*
+ * Quantises the new tokens' K and V rows into their slots, after
+ * ckv_plan_blocks (len already counts them).  Row i of request b (0 <= i <
+ * granted[b]; its position is len[b] - granted[b] + i) is read at
+ *   packed   (T_rows = 0)  k_new + (start[b] + i) * stride_t
+ *   padded   (T_rows > 0)  k_new + b * stride_b + i * stride_t, i < T_rows
+ * plus h * stride_h for KV head h; v_new alike; strides in elements of the
+ * cache's dtype, rows of d contiguous elements, 16-byte aligned.  Requests with
+ * granted[b] <= 0 take no part.
+ * For each block that gets new rows, each head, and K and V apart, with a = the
+ * largest magnitude among the new rows (at least 2^-100):
+ *   int8   s = a / 127;  e4m3   s = the least power of two with a <= 448 s
+ *   if the block already holds rows: s = max(s, its scale), and where that
+ *   raises the scale the older codes become rne(code * (old s * (1/s)))
+ *   code = rne(x * (1/s)), ties to even, |code| <= 127 (int8)
+ * (a/127, 1/s and old s * (1/s) rounded to fp32; the products exact).  The
+ * power of two costs e4m3 nothing and re-scales codes without a second
+ * rounding.  A value that is not finite makes its block's scale NaN (K or V of
+ * that head), and so the attention's output of requests holding the block.
+ * The rest of the pool is left as it was.  One launch.
+ */
+CKV_API ckv_status ckv_quant_append(const ckv_q8_desc* cache, const ckv_plan_desc* plan, const void* k_new,
+                                    const void* v_new, int32_t T_rows, int64_t stride_b, int64_t stride_t,
+                                    int64_t stride_h, ckv_stream_t stream);
+
+/*
+ * Reads rows of the 8-bit cache back in the cache's dtype (code * scale rounded
+ * once): for ckv_build_centroids and ckv_build_edges, which take 16/32-bit
+ * rows, or a prefill attention over what is cached.  Row r (0 <= r < R) of
+ * request b, head h is position first[b] + r (first NULL: 0) and goes to
+ * k_out + b * stride_b + h * stride_h + r * stride_t; positions outside
+ * [0, len[b]) give zeros.  16-byte aligned rows; strides in elements.
+ */
+CKV_API ckv_status ckv_q8_read(const ckv_q8_desc* cache, const int32_t* first, int32_t R, void* k_out, void* v_out,
+                               int64_t stride_b, int64_t stride_h, int64_t stride_t, ckv_stream_t stream);
+
+/*
+ * Workspace of the two attention calls below (graph and sel NULL: the dense
+ * one alone).  Unlike the other calls' it keeps a counter per (request, KV head):
+ * zero-fill the whole workspace once after allocating it, and give it to these
+ * two calls only, with the B and Hkv that it was sized for; every call leaves the
+ * counters zero.  Calls sharing it must not overlap on the GPU (graphs captured
+ * with one workspace included).
+ */
+CKV_API ckv_status ckv_q8_workspace_size(const ckv_q8_desc* cache, const ckv_graph_desc* graph,
+                                         const ckv_selection_desc* sel, size_t* bytes);
+
+/*
+ * ckv_dense_decode over the 8-bit cache: exact softmax attention of one token's
+ * queries q [B, Hq, d] (cache dtype, contiguous) over positions [0, len[b]) of
+ * each request; out fp32 [B, Hq, d], zeros where len[b] = 0.  Codes are exact
+ * in the products, the softmax's statistics and sums are fp32.  One launch.
+ */
+CKV_API ckv_status ckv_dense_decode_q8(const ckv_q8_desc* cache, const void* q, float* out, void* ws, size_t ws_bytes,
+                                       ckv_stream_t stream);
+
+/*
+ * ckv_sparse_decode over the 8-bit cache: the selected positions of sel (from
+ * ckv_score_select, whose cache descriptor then needs shapes only: k = v =
+ * NULL, the graph's T_cap) are read through the block table.  out, nbr8 as
+ * there; entries outside [0, len[b]) or in a bad block are skipped.
+ * k_new [B, Hkv, d] (cache dtype, contiguous) not NULL: the new token, which
+ * will be position len[b] of request b, also joins a community of every
+ * graph unit as in ckv_sparse_decode_append (same rule and results; assigned
+ * as there); its rows are then written by ckv_plan_blocks and
+ * ckv_quant_append.  A request with len[b] >= T_cap joins nothing
+ * (CKV_DEVERR_INDEX).  graph->T_cap <= max_blocks * block.
+ */
+CKV_API ckv_status ckv_sparse_decode_q8(const ckv_q8_desc* cache, const void* q, const ckv_graph_desc* graph,
+                                        const ckv_selection_desc* sel, float* out, int32_t* nbr8, const void* k_new,
+                                        int32_t* assigned, void* ws, size_t ws_bytes, ckv_stream_t stream);
+
+/*
  * Reads the graph's device error word (ckv_graph_desc.dev_err, an OR of
  * CKV_DEVERR_* bits) after everything queued on `stream` so far: the one
  * call that synchronises (it waits for the stream).  *code receives the
  * word; with reset != 0 the word is then set back to zero on the device.
+ * Only graph->dev_err is used: a descriptor holding nothing else reads the
+ * word of an 8-bit cache.
  * NULL graph or code: CKV_ERR_INVALID_ARG; a failed copy or wait:
  * CKV_ERR_CUDA.
  */
@@ -402,7 +577,7 @@ typedef enum {
     CKV_KERNEL_SELECT = 2,     /* no kernel (kept so the kinds keep their numbers) */
     CKV_KERNEL_ATTENTION = 3,  /* split-K attention (sparse and dense decode) */
     CKV_KERNEL_MERGE = 4,      /* merge, neighbours and fused update */
-    CKV_KERNEL_UPDATE = 5,     /* ckv_assign_update / ckv_append_assign */
+    CKV_KERNEL_UPDATE = 5,     /* ckv_assign_update / ckv_append_assign; ckv_plan_blocks, ckv_quant_append, ckv_q8_read */
     CKV_KERNEL_EDGES = 6       /* the four kernels of ckv_build_edges, as one */
 } ckv_kernel_kind;
 #define CKV_KERNEL_KINDS 7
