@@ -32,9 +32,9 @@
 // Statistics.  m0 is the running reference of x (raised when an x passes it by
 // 8), the sum uses p = 2^(x - m0).  The weights carry s_v, whose size the
 // softmax does not know, so they have a reference of their own:
-// w = p c s_v with c a power of two such that w <= 2^7 when set and <= 2^15 at
-// any time (fp16's range); hi + lo then keep 2^-25 of the largest weight's size
-// at worst.  c leaves again, exactly, when a partial is written.
+// w = p c s_v with c a power of two such that w is in (2^4, 2^5] at its largest
+// when set and at most 2^15 at any time (fp16's range); hi + lo then keep 2^-29
+// of the largest weight.  c leaves again, exactly, when a partial is written.
 #pragma once
 
 #include <type_traits>
@@ -71,10 +71,57 @@ __device__ __forceinline__ int q8_swz(int r, int c) {
 
 __device__ __forceinline__ void q8_mma(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0,
                                        unsigned b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void q8_mma0(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0,
+                                        unsigned b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Pairs of fp32 in one 64-bit register, for the packed add and product.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+template <int OFF>
+__device__ __forceinline__ uint4 lds128(unsigned a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4+%5];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a), "n"(OFF) : "memory");
+    return r;
+}
+template <int OFF>
+__device__ __forceinline__ uint2 lds64(unsigned a) {
+    uint2 r;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2+%3];" : "=r"(r.x), "=r"(r.y) : "r"(a), "n"(OFF) : "memory");
+    return r;
+}
+__device__ __forceinline__ float lds32f(unsigned a) {
+    float r;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(a) : "memory");
+    return r;
+}
+__device__ __forceinline__ unsigned smem_addr32(const void* p) {
+    return static_cast<unsigned>(__cvta_generic_to_shared(p));
 }
 __device__ __forceinline__ unsigned q8_transpose(unsigned x) {
     unsigned y;
@@ -89,28 +136,68 @@ __device__ __forceinline__ float2 unpack_half2(unsigned w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// Codes c0..c3 of a word as two fp16 pairs (c0, c1), (c2, c3).  int8: the
-// biased byte is the low part of an fp16 in [1024, 1280), whose step is 1.
+// A K word's four codes as two fp16 pairs, in an order of their own (K_PAIR).
+// int8: bytes 0, 2 and 1, 3, biased by 128, as fp16 subnormals (128 + c) 2^-24:
+// three instructions for four codes.  The bias leaves through the
+// accumulators' start, -128 2^-24 sum q.  e4m3: bytes 0, 1 and 2, 3.
 template <int FMT>
-__device__ __forceinline__ void q8_halves(unsigned w, unsigned& p01, unsigned& p23) {
+__device__ __forceinline__ void q8_k_halves(unsigned w, unsigned& p0, unsigned& p1) {
+    if constexpr (FMT == Q8_I8) {
+        w ^= 0x80808080u;
+        p0 = w & 0x00ff00ffu;
+        p1 = __byte_perm(w, 0u, 0x4341);
+    } else {
+        p0 = e4m3x2_half2((unsigned short)(w & 0xffffu));
+        p1 = e4m3x2_half2((unsigned short)(w >> 16));
+    }
+}
+// Dims of a word's fp16 pairs: pair i holds dims first(i) and first(i) + step.
+template <int FMT> struct KPair {
+    static constexpr int step = FMT == Q8_I8 ? 2 : 1;
+    static constexpr int second = FMT == Q8_I8 ? 1 : 2;  // first(0) = 0
+};
+
+// The words of two tokens (a, b), four dims each: h[i] = fp16 (a_i, b_i).  int8: a
+// byte flipped to 128 + c is the low part of an fp16 in [1024, 1280), whose step is 1;
+// here the bias is taken off (in the sums it would cancel 2^7 of their bits).
+template <int FMT>
+__device__ __forceinline__ void q8_v_halves(unsigned a, unsigned b, unsigned (&h)[4]) {
     if constexpr (FMT == Q8_I8) {
         const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
-        w ^= 0x80808080u;
-        const unsigned a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
-        const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
-        const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
-        p01 = *reinterpret_cast<const unsigned*>(&x);
-        p23 = *reinterpret_cast<const unsigned*>(&y);
+        a ^= 0x80808080u;
+        b ^= 0x80808080u;
+        const unsigned lo = __byte_perm(a, b, 0x5140), hi = __byte_perm(a, b, 0x7362);  // a0 b0 a1 b1, a2 b2 a3 b3
+        const unsigned w[4] = {__byte_perm(lo, 0x64646464u, 0x4140), __byte_perm(lo, 0x64646464u, 0x4342),
+                               __byte_perm(hi, 0x64646464u, 0x4140), __byte_perm(hi, 0x64646464u, 0x4342)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&w[i]), bias);
+            h[i] = *reinterpret_cast<const unsigned*>(&x);
+        }
     } else {
-        p01 = e4m3x2_half2((unsigned short)(w & 0xffffu));
-        p23 = e4m3x2_half2((unsigned short)(w >> 16));
+        const unsigned lo = __byte_perm(a, b, 0x5140), hi = __byte_perm(a, b, 0x7362);  // a0 b0 a1 b1, a2 b2 a3 b3
+        h[0] = e4m3x2_half2((unsigned short)(lo & 0xffffu));
+        h[1] = e4m3x2_half2((unsigned short)(lo >> 16));
+        h[2] = e4m3x2_half2((unsigned short)(hi & 0xffffu));
+        h[3] = e4m3x2_half2((unsigned short)(hi >> 16));
     }
 }
 
-__device__ __forceinline__ void cp_async_4z(void* smem, const void* gmem, bool pred) {
-    unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(smem));
-    int sz = pred ? 4 : 0;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(s), "l"(gmem), "r"(sz) : "memory");
+// 16 bytes to shared address s + SO from g + GO
+template <int SO, int GO>
+__device__ __forceinline__ void cp_async_16i(unsigned s, const void* g) {
+    asm volatile("cp.async.cg.shared.global [%0+%2], [%1+%3], 16;\n" ::"r"(s), "l"(g), "n"(SO), "n"(GO) : "memory");
+}
+__device__ __forceinline__ void cp_async_16s(unsigned s, const void* g, int size) {  // size 0: zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(g), "r"(size) : "memory");
+}
+__device__ __forceinline__ void cp_async_4s(unsigned s, const void* g, int size) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(s), "l"(g), "r"(size) : "memory");
+}
+__device__ __forceinline__ void cp_async_4p(unsigned s, const void* g, bool pred) {  // nothing when !pred
+    asm volatile("{\n.reg .pred p;\nsetp.ne.s32 p, %2, 0;\n@p cp.async.ca.shared.global [%0], [%1], 4;\n}\n" ::"r"(s),
+                 "l"(g), "r"((int)pred)
+                 : "memory");
 }
 
 // The state of one warp over one unit's tokens: lane 4 g + t.
@@ -118,12 +205,13 @@ template <int D, int GQ, int FMT>
 struct Q8Warp {
     using QG = Q8Geom<D>;
     static constexpr bool SPLIT = GQ == 8;  // hi and lo in products of their own
-    unsigned qh[QG::KS][2];                 // Q^T fragments (SPLIT: hi; else hi in columns 0..3, lo in 4..7)
+    unsigned qh[QG::KS][2];                 // Q^T fragments (SPLIT: hi; else hi in columns 0..3, lo or hi again in 4..7)
     unsigned ql[SPLIT ? QG::KS : 1][2];
-    bool q_lo;                              // SPLIT: some lo is not zero (q in fp32)
+    bool q_lo;                              // some lo is not zero (q in fp32)
+    float s0[2];                            // start of the scores' accumulators (int8: the codes' bias taken off)
     float qf[2];                            // per head of this lane: 2^e log2(e)/sqrt(d)
     float m0[2], mw[2], c[2], l[2];         // references of x and of x + log2 s_v, weight factor, sum
-    float o[QG::MT][4];
+    f32x2 o[QG::MT][2];                     // columns 2t, 2t + 1 of rows g and g + 8 of each 16-dim tile
 
     __device__ __forceinline__ static int head(int t, int e) { return SPLIT ? 2 * t + e : (2 * t + e) & 3; }
 
@@ -135,34 +223,44 @@ struct Q8Warp {
             l[e] = 0.f;
         }
 #pragma unroll
-        for (int m = 0; m < QG::MT; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[m][i] = 0.f;
+        for (int m = 0; m < QG::MT; ++m) o[m][0] = o[m][1] = 0ull;
     }
 
     // q: the group's first row.  Lane (g, t) holds column g: head g (SPLIT), or
     // head g & 3, hi for g < 4 and lo otherwise; dims 16 (t + 4 j) + 4 w + 0..3
-    // are k-step 4 j + w.
-    __device__ __forceinline__ void load_q(const void* q, int dtype, float scale_log2, int lane) {
+    // are k-step 4 j + w, in the order of the K word's pairs.  fetch_q only loads, so that the latency of q and of
+    // what the caller loads next overlap.
+    struct RawQ {
+        uint4 w[QG::KS];
+    };
+    __device__ __forceinline__ static RawQ fetch_q(const void* q, int dtype, int lane) {
         const int g = lane >> 2, t = lane & 3;
         const int h = SPLIT ? g : g & 3;
-        const bool real = h < GQ;
+        RawQ r;
+#pragma unroll
+        for (int s = 0; s < QG::KS; ++s) {
+            const int dim = 16 * (t + 4 * (s >> 2)) + 4 * (s & 3);
+            const size_t at = (size_t)(h < GQ ? h : 0) * D + dim;
+            if (dtype == CKV_DTYPE_BF16) {
+                const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(q) + at);
+                r.w[s] = make_uint4(w.x << 16, w.x & 0xffff0000u, w.y << 16, w.y & 0xffff0000u);
+            } else {
+                r.w[s] = *reinterpret_cast<const uint4*>(static_cast<const float*>(q) + at);
+            }
+        }
+        return r;
+    }
+    __device__ __forceinline__ void set_q(const RawQ& r, int dtype, float scale_log2, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+        const bool real = (SPLIT ? g : g & 3) < GQ;
         float x[QG::KS][4];
         unsigned amax = 0;
 #pragma unroll
         for (int s = 0; s < QG::KS; ++s) {
-            const int dim = 16 * (t + 4 * (s >> 2)) + 4 * (s & 3);
-            const size_t at = (size_t)(real ? h : 0) * D + dim;
-            if (dtype == CKV_DTYPE_BF16) {
-                const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(q) + at);
-                x[s][0] = bf16_lo(w.x); x[s][1] = bf16_hi(w.x); x[s][2] = bf16_lo(w.y); x[s][3] = bf16_hi(w.y);
-            } else {
-                const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(q) + at);
-                x[s][0] = w.x; x[s][1] = w.y; x[s][2] = w.z; x[s][3] = w.w;
-            }
+            const unsigned w[4] = {r.w[s].x, r.w[s].y, r.w[s].z, r.w[s].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (!real) x[s][i] = 0.f;
+                x[s][i] = real ? __uint_as_float(w[i]) : 0.f;
                 amax = max(amax, __float_as_uint(x[s][i]) & 0x7fffffffu);
             }
         }
@@ -171,56 +269,87 @@ struct Q8Warp {
         // the row's largest magnitude goes to [2^14, 2^15): codes and sums stay in
         // range, and 2^-29 of it is still a normal fp16.  Rows below 2^-100 count
         // as that large.
-        const int e = max((int)(amax >> 23), 27) - 127 - 14;  // amax = m 2^(e + 14)
-        const float down = __uint_as_float((unsigned)(127 - min(e, 126)) << 23);
-        const float f = __uint_as_float((unsigned)(127 + min(max(e, -126), 126)) << 23) * scale_log2;
-        bool any_lo = false;
+        const int e = max((int)(amax >> 23), 27) - 127 - 14;  // amax = m 2^(e + 14), e in [-114, 114]
+        const float down = __uint_as_float((unsigned)(127 - e) << 23);
+        const float f = __uint_as_float((unsigned)(127 + e) << 23) * scale_log2;
+        using KP = KPair<FMT>;
+        float sum = 0.f;
 #pragma unroll
-        for (int s = 0; s < QG::KS; ++s) {
-            unsigned hi[2], lo[2];
+        for (int s = 0; s < QG::KS; ++s)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float a = x[s][2 * i] * down, b = x[s][2 * i + 1] * down;
-                hi[i] = pack_half2(a, b);
-                const float2 r = unpack_half2(hi[i]);
-                lo[i] = pack_half2(a - r.x, b - r.y);
-                if constexpr (SPLIT) {
-                    qh[s][i] = hi[i];
-                    ql[s][i] = lo[i];
-                    any_lo = any_lo || lo[i] != 0u;
-                } else {
-                    qh[s][i] = g < 4 ? hi[i] : lo[i];
+                x[s][KP::second * i] *= down;
+                x[s][KP::second * i + KP::step] *= down;
+                qh[s][i] = pack_half2(x[s][KP::second * i], x[s][KP::second * i + KP::step]);
+            }
+        // bf16 rows are exact in one fp16; without lo parts columns 4..7 repeat 0..3,
+        // and no lane has to fetch the scores of its weights' heads
+        q_lo = dtype == CKV_DTYPE_F32;
+        if (q_lo) {
+#pragma unroll
+            for (int s = 0; s < QG::KS; ++s)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 h2 = unpack_half2(qh[s][i]);
+                    const unsigned lo = pack_half2(x[s][KP::second * i] - h2.x, x[s][KP::second * i + KP::step] - h2.y);
+                    if constexpr (SPLIT) ql[s][i] = lo;
+                    else if (g >= 4) qh[s][i] = lo;
                 }
+        }
+        if constexpr (FMT == Q8_I8) {
+#pragma unroll
+            for (int s = 0; s < QG::KS; ++s)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 h2 = unpack_half2(qh[s][i]);
+                    sum += h2.x + h2.y;
+                    if (SPLIT && q_lo) {
+                        const float2 l2 = unpack_half2(ql[SPLIT ? s : 0][i]);
+                        sum += l2.x + l2.y;
+                    }
+                }
+            sum += __shfl_xor_sync(FULL, sum, 1);
+            sum += __shfl_xor_sync(FULL, sum, 2);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            qf[k] = __shfl_sync(FULL, f, head(t, k) * 4);
+            s0[k] = 0.f;
+            if constexpr (FMT == Q8_I8) {
+                s0[k] = -0x1p-17f * __shfl_sync(FULL, sum, (2 * t + k) * 4);
+                qf[k] *= 0x1p24f;
             }
         }
-        q_lo = SPLIT && __any_sync(FULL, any_lo);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) qf[k] = __shfl_sync(FULL, f, head(t, k) * 4);
+    }
+    __device__ __forceinline__ static const void* q_row(const void* q, int dtype, size_t row) {
+        return static_cast<const char*>(q) + row * D * (dtype == CKV_DTYPE_BF16 ? 2 : 4);
     }
 
-    // One staged tile.  lam (NEIGHBOURS): lam(i, x) receives the largest x over
-    // the group's heads of the tile's token i, from one lane per token.
-    template <bool NEIGHBOURS, typename Lam>
-    __device__ __forceinline__ void tile(const unsigned char* sm, int lane, Lam lam) {
+    // One tile staged at sm; mask: which of its tokens count.  UNIFORM: all its tokens have one scale each for K and V.
+    // lam (NEIGHBOURS): lam(i, x) receives the largest x over the group's heads
+    // of the tile's token i, from one lane per token.
+    template <bool UNIFORM, bool NEIGHBOURS, typename Lam>
+    __device__ __forceinline__ void tile(unsigned sm, unsigned mask, int lane, Lam lam) {
         const int g = lane >> 2, t = lane & 3;
-        const unsigned mask = *reinterpret_cast<const unsigned*>(sm + QG::MASK);
         if (mask == 0u) return;  // uniform over the warp
-        const float* sc = reinterpret_cast<const float*>(sm + QG::SCALES);
+        // rows 8 apart are 8 D bytes apart; chunks t and t + 4 (d = 128) differ in bit 6,
+        // and so do, a row on, rows 2t and 2t + 1
+        const unsigned ks = sm + q8_swz<D>(g, t), ks2 = sm + (q8_swz<D>(g, t) ^ 64);
 
         // S: rows g, g + 8, columns 2t, 2t + 1; even and odd k-steps apart
-        float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+        float sa[4] = {s0[0], s0[1], s0[0], s0[1]}, sb[4];
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
-            const uint4 ka = *reinterpret_cast<const uint4*>(sm + q8_swz<D>(g, t + 4 * j));
-            const uint4 kb = *reinterpret_cast<const uint4*>(sm + q8_swz<D>(g + 8, t + 4 * j));
+            const uint4 ka = lds128<0>(j ? ks2 : ks), kb = lds128<8 * D>(j ? ks2 : ks);
             const unsigned wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 const int s = 4 * j + w;
                 unsigned a0, a1, a2, a3;
-                q8_halves<FMT>(wa[w], a0, a2);
-                q8_halves<FMT>(wb[w], a1, a3);
-                q8_mma((w & 1) ? sb : sa, a0, a1, a2, a3, qh[s][0], qh[s][1]);
+                q8_k_halves<FMT>(wa[w], a0, a2);
+                q8_k_halves<FMT>(wb[w], a1, a3);
+                if (s == 1) q8_mma0(sb, a0, a1, a2, a3, qh[s][0], qh[s][1]);
+                else q8_mma((w & 1) ? sb : sa, a0, a1, a2, a3, qh[s][0], qh[s][1]);
                 if constexpr (SPLIT) {
                     if (q_lo) q8_mma((w & 1) ? sb : sa, a0, a1, a2, a3, ql[s][0], ql[s][1]);
                 }
@@ -228,18 +357,31 @@ struct Q8Warp {
         }
         float s[2][2];  // [token g | g + 8][head]
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float x = sa[i] + sb[i];
-            if constexpr (!SPLIT) x += __shfl_xor_sync(FULL, x, 2);
-            s[i >> 1][i & 1] = x;
+        for (int i = 0; i < 4; ++i) s[i >> 1][i & 1] = sa[i] + sb[i];
+        if (!SPLIT && q_lo) {  // uniform
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i >> 1][i & 1] += __shfl_xor_sync(FULL, s[i >> 1][i & 1], 2);
         }
-        const float ks[2] = {sc[g], sc[g + 8]}, vs[2] = {sc[16 + g], sc[24 + g]};
+        constexpr int NS = UNIFORM ? 1 : 2;
+        float vs[NS], kf[NS][2];
+#pragma unroll
+        for (int r = 0; r < NS; ++r) {
+            const int at = UNIFORM ? 0 : g + 8 * r;
+            vs[r] = lds32f(sm + QG::SCALES + 64 + 4 * at);
+            const float kscale = lds32f(sm + QG::SCALES + 4 * at);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) kf[r][e] = kscale * qf[e];
+        }
         const bool on[2] = {(mask >> g & 1u) != 0u, (mask >> (g + 8) & 1u) != 0u};
-        float kf[2][2];
+        if (mask != 0xffffu) {  // uniform
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) kf[r][e] = ks[r] * qf[e];
+                for (int e = 0; e < 2; ++e) {
+                    s[r][e] = on[r] ? s[r][e] : -INFINITY;
+                    if (!UNIFORM) kf[r % NS][e] = on[r] ? kf[r % NS][e] : 1.f;  // its scale was not copied
+                }
+        }
 
         if constexpr (NEIGHBOURS) {
 #pragma unroll
@@ -247,7 +389,7 @@ struct Q8Warp {
                 float v = -INFINITY;
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    if (head(t, e) < GQ && on[r]) v = fmaxf(v, s[r][e] * kf[r][e]);
+                    if (head(t, e) < GQ && on[r]) v = fmaxf(v, s[r][e] * kf[r % NS][e]);
                 v = fmaxf(v, __shfl_xor_sync(FULL, v, 1));
                 if constexpr (SPLIT) v = fmaxf(v, __shfl_xor_sync(FULL, v, 2));
                 if (t == 0) lam(g + 8 * r, v);
@@ -256,30 +398,45 @@ struct Q8Warp {
 
         float p[2][2], w[2][2];
         auto weights = [&]() {
-            bool high = false;
+            float cv[NS][2];
+            bool high = false, wide = false;
+#pragma unroll
+            for (int r = 0; r < NS; ++r)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    cv[r][e] = fminf(c[e] * vs[r], 0x1p127f);  // finite: a weight of zero stays one
+                    wide = wide || cv[r][e] > 128.f;
+                }
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     // one rounding for x - m0: the largest weights are the most exact
-                    const float y = on[r] ? fmaf(s[r][e], kf[r][e], -m0[e]) : -INFINITY;
+                    const float y = fmaf(s[r][e], kf[r % NS][e], -m0[e]);
                     p[r][e] = exp2_approx(y);
-                    w[r][e] = p[r][e] * c[e] * vs[r];
-                    high = high || y > 8.f || w[r][e] > 32768.f;
+                    w[r][e] = p[r][e] * cv[r % NS][e];
+                    high = high || p[r][e] > 256.f;
                 }
+            if (__any_sync(FULL, wide)) {  // with p <= 2^8 only these can pass 2^15
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) high = high || w[r][e] > 32768.f;
+            }
             return __any_sync(FULL, high);
         };
         if (weights()) {
             // raise the references to this tile's largest values
+            float fo[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float mx = Q8_M_INIT, mv = Q8_M_INIT;
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float x = s[r][e] * kf[r][e];
+                    const float x = s[r][e] * kf[r % NS][e];
                     if (on[r]) {
                         mx = fmaxf(mx, x);
-                        mv = fmaxf(mv, x + __log2f(vs[r]));
+                        mv = fmaxf(mv, x + __log2f(vs[r % NS]));
                     }
                 }
 #pragma unroll
@@ -289,23 +446,24 @@ struct Q8Warp {
                 }
                 const float mn = fmaxf(m0[e], mx);
                 mw[e] = fmaxf(mw[e], mv);
-                const int k2 = (int)fminf(fmaxf(7.f - ceilf(mw[e] - mn), -120.f), 120.f);
+                const int k2 = (int)fminf(fmaxf(5.f - ceilf(mw[e] - mn), -120.f), 120.f);
                 const float cn = __uint_as_float((unsigned)(127 + k2) << 23);
                 const float f = exp2_approx(m0[e] - mn);
-                const float fo = f * (cn / c[e]);
+                fo[e] = f * (cn / c[e]);
                 m0[e] = mn;
                 c[e] = cn;
                 l[e] *= f;
+            }
+            const f32x2 f2 = pack2(fo[0], fo[1]);
 #pragma unroll
-                for (int m = 0; m < QG::MT; ++m) {
-                    o[m][e] *= fo;
-                    o[m][2 + e] *= fo;
-                }
+            for (int m = 0; m < QG::MT; ++m) {
+                o[m][0] = mul2(o[m][0], f2);
+                o[m][1] = mul2(o[m][1], f2);
             }
             weights();
         }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) l[e] += p[0][e] + p[1][e];
+        l[0] += p[0][0] + p[1][0];
+        l[1] += p[0][1] + p[1][1];
 
         // P fragments: token pairs of column g
         unsigned b[SPLIT ? 2 : 1][2];
@@ -323,31 +481,41 @@ struct Q8Warp {
         }
         // O: lane's codes are dims (d/8) g + 0..d/8-1 of tokens 2t, 2t+1, 2t+8, 2t+9
         unsigned vw[4][D / 32];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int r = 2 * t + (k & 1) + 8 * (k >> 1);
+        {
+            constexpr int T = QG::TILE, N = 8 * D;  // 8 rows on
             if constexpr (D == 128) {
-                const uint4 x = *reinterpret_cast<const uint4*>(sm + QG::TILE + q8_swz<D>(r, g));
-                vw[k][0] = x.x; vw[k][1] = x.y; vw[k][2] = x.z; vw[k][3] = x.w;
+                const unsigned v0 = sm + q8_swz<D>(2 * t, g), v1 = sm + (q8_swz<D>(2 * t, g) ^ 64);
+                const uint4 x[4] = {lds128<T>(v0), lds128<T + 128>(v1), lds128<T + N>(v0), lds128<T + N + 128>(v1)};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    vw[k][0] = x[k].x; vw[k][1] = x[k].y; vw[k][2] = x[k].z; vw[k][3] = x[k].w;
+                }
             } else {
-                const uint2 x = *reinterpret_cast<const uint2*>(sm + QG::TILE + q8_swz<D>(r, g >> 1) + 8 * (g & 1));
-                vw[k][0] = x.x; vw[k][1] = x.y;
+                const unsigned v0 = sm + q8_swz<D>(2 * t, g >> 1) + 8 * (g & 1);
+                const unsigned v1 = sm + (q8_swz<D>(2 * t, g >> 1) ^ 64) + 8 * (g & 1);
+                const uint2 x[4] = {lds64<T>(v0), lds64<T>(v1), lds64<T + N>(v0), lds64<T + N>(v1)};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    vw[k][0] = x[k].x; vw[k][1] = x[k].y;
+                }
             }
         }
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-            // bytes of two tokens interleaved, then the pairs' fp16
-            unsigned a[2][4];  // [tokens 2t | 2t + 8][code of the word]
+            unsigned a[2][4];  // [tokens 2t, 2t + 1 | 2t + 8, 2t + 9][code of the word]
+            q8_v_halves<FMT>(vw[0][i], vw[1][i], a[0]);
+            q8_v_halves<FMT>(vw[2][i], vw[3][i], a[1]);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                q8_halves<FMT>(__byte_perm(vw[2 * k][i], vw[2 * k + 1][i], 0x5140), a[k][0], a[k][1]);
-                q8_halves<FMT>(__byte_perm(vw[2 * k][i], vw[2 * k + 1][i], 0x7362), a[k][2], a[k][3]);
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                q8_mma(o[2 * i + k], a[0][2 * k], a[0][2 * k + 1], a[1][2 * k], a[1][2 * k + 1], b[0][0], b[0][1]);
+                // a tile's products start from zero and are added in fp32: the
+                // tensor core truncates its sums, which over the hundreds of
+                // tiles of a long request would cost 4e-6 of the output
+                float d[4];
+                q8_mma0(d, a[0][2 * k], a[0][2 * k + 1], a[1][2 * k], a[1][2 * k + 1], b[0][0], b[0][1]);
                 if constexpr (SPLIT)
-                    q8_mma(o[2 * i + k], a[0][2 * k], a[0][2 * k + 1], a[1][2 * k], a[1][2 * k + 1], b[1][0], b[1][1]);
+                    q8_mma(d, a[0][2 * k], a[0][2 * k + 1], a[1][2 * k], a[1][2 * k + 1], b[1][0], b[1][1]);
+                o[2 * i + k][0] = add2(o[2 * i + k][0], pack2(d[0], d[1]));
+                o[2 * i + k][1] = add2(o[2 * i + k][1], pack2(d[2], d[3]));
             }
         }
     }
@@ -362,9 +530,10 @@ struct Q8Warp {
         const float inv[2] = {1.f / c[0], 1.f / c[1]};
 #pragma unroll
         for (int i = 0; i < QG::MT; ++i) {
+            const float2 x = unpack2(o[i][0]), y = unpack2(o[i][1]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float a = o[i][e] * inv[e], b = o[i][2 + e] * inv[e];
+                float a = (e ? x.y : x.x) * inv[e], b = (e ? y.y : y.x) * inv[e];
                 if constexpr (!SPLIT) {
                     a += __shfl_xor_sync(FULL, a, 2);
                     b += __shfl_xor_sync(FULL, b, 2);

@@ -36,6 +36,9 @@ __device__ __forceinline__ void sparse_q8_segment(const SparseQ8Params& p, int u
     const int len = (int)min((long long)t.len[b], (long long)t.max_blocks << t.sh);
     const int n = hi - lo, nit = (n + Q8_TOK - 1) / Q8_TOK;
 
+    const auto raw_q = Q8Warp<D, GQ, FMT>::fetch_q(
+        Q8Warp<D, GQ, FMT>::q_row(p.d.q, p.c.dtype, (size_t)b * p.d.Hq + h0), p.c.dtype, lane);
+
     // windows of 32 list entries (two tiles): positions two windows ahead of the
     // copies, pool rows (-1: not attended) one window ahead
     auto positions = [&](int w) { return w * 32 + lane < n ? toks[lo + w * 32 + lane] : -1; };
@@ -61,23 +64,24 @@ __device__ __forceinline__ void sparse_q8_segment(const SparseQ8Params& p, int u
                 row_nxt = rows(pos_nxt, w + 1);
                 pos_nxt = positions(w + 2);
             }
-            unsigned char* sm = ring + stage_in * QG::SLOT;
+            unsigned char* slot_p = ring + stage_in * QG::SLOT;
+            const unsigned sm = smem_addr32(slot_p);
             const int base = (i & 1) << 4;
 #pragma unroll
             for (int x = 0; x < QG::TILE / 512; ++x) {
                 const int idx = x * 32 + lane, r = idx / QG::CH, c = idx % QG::CH;
                 const int row = __shfl_sync(FULL, row_cur, base + r);
-                const bool ok = row >= 0;
-                const int64_t src = (int64_t)(ok ? row : 0) * D + c * 16;
-                const int dst = q8_swz<D>(r, c);
-                cp_async_16(sm + dst, static_cast<const char*>(p.c.k) + src, ok);
-                cp_async_16(sm + QG::TILE + dst, static_cast<const char*>(p.c.v) + src, ok);
+                const int size = row >= 0 ? 16 : 0;
+                const size_t src = (size_t)max(row, 0) * D + c * 16;
+                const unsigned dst = sm + q8_swz<D>(r, c);
+                cp_async_16s(dst, static_cast<const char*>(p.c.k) + src, size);
+                cp_async_16s(dst + QG::TILE, static_cast<const char*>(p.c.v) + src, size);
             }
             const int row = __shfl_sync(FULL, row_cur, base + (lane & 15));
-            cp_async_4z(sm + QG::SCALES + lane * 4, (lane < 16 ? p.c.k_scale : p.c.v_scale) + (max(row, 0) >> t.sh),
-                        row >= 0);
+            cp_async_4s(sm + QG::SCALES + lane * 4, (lane < 16 ? p.c.k_scale : p.c.v_scale) + (max(row, 0) >> t.sh),
+                        row >= 0 ? 4 : 0);
             const unsigned mask = __ballot_sync(FULL, row >= 0) & 0xffffu;
-            if (lane == 0) *reinterpret_cast<unsigned*>(sm + QG::MASK) = mask;
+            if (lane == 0) *reinterpret_cast<unsigned*>(slot_p + QG::MASK) = mask;
         }
         stage_in = stage_in + 1 == QS_STAGES ? 0 : stage_in + 1;
         cp_async_commit();
@@ -85,8 +89,7 @@ __device__ __forceinline__ void sparse_q8_segment(const SparseQ8Params& p, int u
 #pragma unroll
     for (int s = 0; s < QS_STAGES - 1; ++s) issue(s);
     Q8Warp<D, GQ, FMT> st;
-    st.load_q(static_cast<const char*>(p.d.q) + ((size_t)b * p.d.Hq + h0) * D * (p.c.dtype == CKV_DTYPE_BF16 ? 2 : 4),
-              p.c.dtype, p.d.scale_log2, lane);
+    st.set_q(raw_q, p.c.dtype, p.d.scale_log2, lane);
     st.reset();
     float* lamu = p.d.ws.lam + (size_t)u * p.d.ws.lam_cap + lo;
     int stage_out = 0;
@@ -97,12 +100,12 @@ __device__ __forceinline__ void sparse_q8_segment(const SparseQ8Params& p, int u
             cp_async_wait<QS_STAGES - 1>();
             __syncwarp();  // what the other lanes copied is visible
             const unsigned char* sm = ring + stage_out * QG::SLOT;
+            const unsigned mask = *reinterpret_cast<const unsigned*>(sm + QG::MASK);
             if constexpr (decltype(nbr)::value) {
                 // an all-invalid tile has no logits of its own to store
-                if (*reinterpret_cast<const unsigned*>(sm + QG::MASK) == 0u && lane < 16 && i * Q8_TOK + lane < n)
-                    lamu[i * Q8_TOK + lane] = -INFINITY;
+                if (mask == 0u && lane < 16 && i * Q8_TOK + lane < n) lamu[i * Q8_TOK + lane] = -INFINITY;
             }
-            st.template tile<decltype(nbr)::value>(sm, lane, [&](int k, float x) {
+            st.template tile<false, decltype(nbr)::value>(smem_addr32(sm), mask, lane, [&](int k, float x) {
                 if (i * Q8_TOK + k < n) lamu[i * Q8_TOK + k] = x;
             });
             stage_out = stage_out + 1 == QS_STAGES ? 0 : stage_out + 1;
