@@ -44,21 +44,23 @@
 
 namespace ckv {
 
-constexpr int Q8_TOK = 16;  // tokens of a tile
+constexpr int Q8_HALF = 16;  // tokens of a product's tile
+constexpr int Q8_TOK = 32;   // tokens of a staged tile: two of those
 constexpr float Q8_M_INIT = -1e30f;
 
 template <int D>
 struct Q8Geom {
-    static constexpr int TILE = Q8_TOK * D;        // bytes of a K or V tile
+    static constexpr int HALF = Q8_HALF * D;       // bytes of 16 rows
+    static constexpr int V = 2 * HALF;             // K's two halves, then V's
     static constexpr int CH = D / 16;              // 16-byte chunks per row
-    static constexpr int SCALES = 2 * TILE;        // float [16] of K, then of V
-    static constexpr int MASK = SCALES + 128;      // 16 bits: the tokens that count
-    static constexpr int SLOT = SCALES + 256;      // bytes of a ring slot (a multiple of 128)
+    static constexpr int SCALES = 4 * HALF;        // float [32] of K, then of V
+    static constexpr int MASK = SCALES + 256;      // 32 bits (sparse): the tokens that count
+    static constexpr int SLOT = SCALES + 384;      // bytes of a ring slot (a multiple of 128)
     static constexpr int KS = D / 16;              // k-steps of Q K^T
     static constexpr int MT = D / 16;              // 16-dim tiles of V^T
 };
 
-// Byte offset of 16-byte chunk c of token row r in a staged tile.  Q K^T reads
+// Byte offset of 16-byte chunk c of token row r in 16 staged rows.  Q K^T reads
 // chunk t (t+4) of rows g, 8 lanes at a time: rows 2i, 2i+1 x 4 chunks; P V reads
 // d/8 bytes at chunk position g of rows 2t (2t+1, 2t+8, 2t+9): 4 even or odd
 // rows x the chunks of 2 (d = 128) or 4 (d = 64, 8-byte reads) values of g.
@@ -325,9 +327,11 @@ struct Q8Warp {
         return static_cast<const char*>(q) + row * D * (dtype == CKV_DTYPE_BF16 ? 2 : 4);
     }
 
-    // One tile staged at sm; mask: which of its tokens count.  UNIFORM: all its tokens have one scale each for K and V.
-    // lam (NEIGHBOURS): lam(i, x) receives the largest x over the group's heads
-    // of the tile's token i, from one lane per token.
+    // One tile staged at sm; mask: which of its tokens count.  UNIFORM: the 16
+    // tokens of a half have one scale each for K and V.  lam (NEIGHBOURS): lam(i, x)
+    // receives the largest x over the group's heads of the tile's token i, from
+    // one lane per token.  Two halves at a time give the products independent work
+    // and share the checks, the loads' bookkeeping and the fp32 additions.
     template <bool UNIFORM, bool NEIGHBOURS, typename Lam>
     __device__ __forceinline__ void tile(unsigned sm, unsigned mask, int lane, Lam lam) {
         const int g = lane >> 2, t = lane & 3;
@@ -336,92 +340,105 @@ struct Q8Warp {
         // and so do, a row on, rows 2t and 2t + 1
         const unsigned ks = sm + q8_swz<D>(g, t), ks2 = sm + (q8_swz<D>(g, t) ^ 64);
 
-        // S: rows g, g + 8, columns 2t, 2t + 1; even and odd k-steps apart
-        float sa[4] = {s0[0], s0[1], s0[0], s0[1]}, sb[4];
+        // S: rows g, g + 8 of each half, columns 2t, 2t + 1; even and odd k-steps apart
+        float s[2][2][2];  // [half][token g | g + 8][head]
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-            const uint4 ka = lds128<0>(j ? ks2 : ks), kb = lds128<8 * D>(j ? ks2 : ks);
-            const unsigned wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+        for (int j = 0; j < 2; ++j) {
+            float sa[4] = {s0[0], s0[1], s0[0], s0[1]}, sb[4];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const int s = 4 * j + w;
-                unsigned a0, a1, a2, a3;
-                q8_k_halves<FMT>(wa[w], a0, a2);
-                q8_k_halves<FMT>(wb[w], a1, a3);
-                if (s == 1) q8_mma0(sb, a0, a1, a2, a3, qh[s][0], qh[s][1]);
-                else q8_mma((w & 1) ? sb : sa, a0, a1, a2, a3, qh[s][0], qh[s][1]);
-                if constexpr (SPLIT) {
-                    if (q_lo) q8_mma((w & 1) ? sb : sa, a0, a1, a2, a3, ql[s][0], ql[s][1]);
+            for (int i = 0; i < D / 64; ++i) {
+                const uint4 ka = j ? lds128<QG::HALF>(i ? ks2 : ks) : lds128<0>(i ? ks2 : ks);
+                const uint4 kb = j ? lds128<QG::HALF + 8 * D>(i ? ks2 : ks) : lds128<8 * D>(i ? ks2 : ks);
+                const unsigned wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int k = 4 * i + w;
+                    unsigned a0, a1, a2, a3;
+                    q8_k_halves<FMT>(wa[w], a0, a2);
+                    q8_k_halves<FMT>(wb[w], a1, a3);
+                    if (k == 1) q8_mma0(sb, a0, a1, a2, a3, qh[k][0], qh[k][1]);
+                    else q8_mma((w & 1) ? sb : sa, a0, a1, a2, a3, qh[k][0], qh[k][1]);
+                    if constexpr (SPLIT) {
+                        if (q_lo) q8_mma((w & 1) ? sb : sa, a0, a1, a2, a3, ql[k][0], ql[k][1]);
+                    }
                 }
             }
-        }
-        float s[2][2];  // [token g | g + 8][head]
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[i >> 1][i & 1] = sa[i] + sb[i];
+            for (int i = 0; i < 4; ++i) s[j][i >> 1][i & 1] = sa[i] + sb[i];
+        }
         if (!SPLIT && q_lo) {  // uniform
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[i >> 1][i & 1] += __shfl_xor_sync(FULL, s[i >> 1][i & 1], 2);
+            for (int i = 0; i < 8; ++i)
+                s[i >> 2][i >> 1 & 1][i & 1] += __shfl_xor_sync(FULL, s[i >> 2][i >> 1 & 1][i & 1], 2);
         }
         constexpr int NS = UNIFORM ? 1 : 2;
-        float vs[NS], kf[NS][2];
+        float vs[2][NS], kf[2][NS][2];
 #pragma unroll
-        for (int r = 0; r < NS; ++r) {
-            const int at = UNIFORM ? 0 : g + 8 * r;
-            vs[r] = lds32f(sm + QG::SCALES + 64 + 4 * at);
-            const float kscale = lds32f(sm + QG::SCALES + 4 * at);
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) kf[r][e] = kscale * qf[e];
-        }
-        const bool on[2] = {(mask >> g & 1u) != 0u, (mask >> (g + 8) & 1u) != 0u};
-        if (mask != 0xffffu) {  // uniform
+            for (int r = 0; r < NS; ++r) {
+                const unsigned at = sm + QG::SCALES + 64 * j + (UNIFORM ? 0 : 4 * (g + 8 * r));
+                const float kscale = lds32f(at);
+                vs[j][r] = lds32f(at + 128);
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+                for (int e = 0; e < 2; ++e) kf[j][r][e] = kscale * qf[e];
+            }
+        auto on = [&](int j, int r) { return (mask >> (16 * j + 8 * r + g) & 1u) != 0u; };
+        if (mask != 0xffffffffu) {  // uniform
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    s[r][e] = on[r] ? s[r][e] : -INFINITY;
-                    if (!UNIFORM) kf[r % NS][e] = on[r] ? kf[r % NS][e] : 1.f;  // its scale was not copied
-                }
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        s[j][r][e] = on(j, r) ? s[j][r][e] : -INFINITY;
+                        // scales that were not copied are zero
+                        kf[j][r % NS][e] = kf[j][r % NS][e] == 0.f ? 1.f : kf[j][r % NS][e];
+                    }
         }
 
         if constexpr (NEIGHBOURS) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float v = -INFINITY;
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (head(t, e) < GQ && on[r]) v = fmaxf(v, s[r][e] * kf[r % NS][e]);
-                v = fmaxf(v, __shfl_xor_sync(FULL, v, 1));
-                if constexpr (SPLIT) v = fmaxf(v, __shfl_xor_sync(FULL, v, 2));
-                if (t == 0) lam(g + 8 * r, v);
-            }
+                for (int r = 0; r < 2; ++r) {
+                    float v = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (head(t, e) < GQ) v = fmaxf(v, s[j][r][e] * kf[j][r % NS][e]);
+                    v = fmaxf(v, __shfl_xor_sync(FULL, v, 1));
+                    if constexpr (SPLIT) v = fmaxf(v, __shfl_xor_sync(FULL, v, 2));
+                    if (t == 0) lam(16 * j + 8 * r + g, v);
+                }
         }
 
-        float p[2][2], w[2][2];
+        float p[2][2][2], w[2][2][2];
         auto weights = [&]() {
-            float cv[NS][2];
+            float cv[2][NS][2];
             bool high = false, wide = false;
 #pragma unroll
-            for (int r = 0; r < NS; ++r)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    cv[r][e] = fminf(c[e] * vs[r], 0x1p127f);  // finite: a weight of zero stays one
-                    wide = wide || cv[r][e] > 128.f;
-                }
+                for (int r = 0; r < NS; ++r)
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+                    for (int e = 0; e < 2; ++e) {
+                        cv[j][r][e] = fminf(c[e] * vs[j][r], 0x1p127f);  // finite: a weight of zero stays one
+                        wide = wide || cv[j][r][e] > 128.f;
+                    }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    // one rounding for x - m0: the largest weights are the most exact
-                    const float y = fmaf(s[r][e], kf[r % NS][e], -m0[e]);
-                    p[r][e] = exp2_approx(y);
-                    w[r][e] = p[r][e] * cv[r % NS][e];
-                    high = high || p[r][e] > 256.f;
-                }
-            if (__any_sync(FULL, wide)) {  // with p <= 2^8 only these can pass 2^15
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) high = high || w[r][e] > 32768.f;
+                    for (int e = 0; e < 2; ++e) {
+                        // one rounding for x - m0: the largest weights are the most exact
+                        p[j][r][e] = exp2_approx(fmaf(s[j][r][e], kf[j][r % NS][e], -m0[e]));
+                        w[j][r][e] = p[j][r][e] * cv[j][r % NS][e];
+                        high = high || p[j][r][e] > 256.f;
+                    }
+            if (__any_sync(FULL, wide)) {  // with p <= 2^8 only these can pass 2^15
+#pragma unroll
+                for (int i = 0; i < 8; ++i) high = high || w[i >> 2][i >> 1 & 1][i & 1] > 32768.f;
             }
             return __any_sync(FULL, high);
         };
@@ -432,13 +449,15 @@ struct Q8Warp {
             for (int e = 0; e < 2; ++e) {
                 float mx = Q8_M_INIT, mv = Q8_M_INIT;
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float x = s[r][e] * kf[r % NS][e];
-                    if (on[r]) {
-                        mx = fmaxf(mx, x);
-                        mv = fmaxf(mv, x + __log2f(vs[r % NS]));
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float x = s[j][r][e] * kf[j][r % NS][e];
+                        if (on(j, r)) {
+                            mx = fmaxf(mx, x);
+                            mv = fmaxf(mv, x + __log2f(vs[j][r % NS]));
+                        }
                     }
-                }
 #pragma unroll
                 for (int k = 4; k <= 16; k <<= 1) {
                     mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, k));
@@ -462,58 +481,74 @@ struct Q8Warp {
             }
             weights();
         }
-        l[0] += p[0][0] + p[1][0];
-        l[1] += p[0][1] + p[1][1];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) l[e] += (p[0][0][e] + p[0][1][e]) + (p[1][0][e] + p[1][1][e]);
 
         // P fragments: token pairs of column g
-        unsigned b[SPLIT ? 2 : 1][2];
+        unsigned b[2][SPLIT ? 2 : 1][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const unsigned hi = pack_half2(w[r][0], w[r][1]);
-            const float2 back = unpack_half2(hi);
-            const unsigned lo = pack_half2(w[r][0] - back.x, w[r][1] - back.y);
-            if constexpr (SPLIT) {
-                b[0][r] = q8_transpose(hi);
-                b[1][r] = q8_transpose(lo);
-            } else {
-                b[0][r] = q8_transpose(t < 2 ? hi : lo);
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const unsigned hi = pack_half2(w[j][r][0], w[j][r][1]);
+                const float2 back = unpack_half2(hi);
+                const unsigned lo = pack_half2(w[j][r][0] - back.x, w[j][r][1] - back.y);
+                if constexpr (SPLIT) {
+                    b[j][0][r] = q8_transpose(hi);
+                    b[j][1][r] = q8_transpose(lo);
+                } else {
+                    b[j][0][r] = q8_transpose(t < 2 ? hi : lo);
+                }
             }
-        }
-        // O: lane's codes are dims (d/8) g + 0..d/8-1 of tokens 2t, 2t+1, 2t+8, 2t+9
-        unsigned vw[4][D / 32];
+        // O: lane's codes are dims (d/8) g + 0..d/8-1 of tokens 2t, 2t+1, 2t+8, 2t+9 of each half
+        unsigned vw[2][4][D / 32];
         {
-            constexpr int T = QG::TILE, N = 8 * D;  // 8 rows on
+            constexpr int N = 8 * D, H = QG::HALF;  // 8 rows on; the other half
             if constexpr (D == 128) {
-                const unsigned v0 = sm + q8_swz<D>(2 * t, g), v1 = sm + (q8_swz<D>(2 * t, g) ^ 64);
-                const uint4 x[4] = {lds128<T>(v0), lds128<T + 128>(v1), lds128<T + N>(v0), lds128<T + N + 128>(v1)};
+                const unsigned v0 = sm + QG::V + q8_swz<D>(2 * t, g), v1 = sm + QG::V + (q8_swz<D>(2 * t, g) ^ 64);
+                const uint4 x[8] = {lds128<0>(v0),     lds128<128>(v1),     lds128<N>(v0),     lds128<N + 128>(v1),
+                                    lds128<H>(v0),     lds128<H + 128>(v1), lds128<H + N>(v0), lds128<H + N + 128>(v1)};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    vw[k][0] = x[k].x; vw[k][1] = x[k].y; vw[k][2] = x[k].z; vw[k][3] = x[k].w;
+                for (int k = 0; k < 8; ++k) {
+                    vw[k >> 2][k & 3][0] = x[k].x; vw[k >> 2][k & 3][1] = x[k].y;
+                    vw[k >> 2][k & 3][2] = x[k].z; vw[k >> 2][k & 3][3] = x[k].w;
                 }
             } else {
-                const unsigned v0 = sm + q8_swz<D>(2 * t, g >> 1) + 8 * (g & 1);
-                const unsigned v1 = sm + (q8_swz<D>(2 * t, g >> 1) ^ 64) + 8 * (g & 1);
-                const uint2 x[4] = {lds64<T>(v0), lds64<T>(v1), lds64<T + N>(v0), lds64<T + N>(v1)};
+                const unsigned v0 = sm + QG::V + q8_swz<D>(2 * t, g >> 1) + 8 * (g & 1);
+                const unsigned v1 = sm + QG::V + (q8_swz<D>(2 * t, g >> 1) ^ 64) + 8 * (g & 1);
+                const uint2 x[8] = {lds64<0>(v0), lds64<0>(v1), lds64<N>(v0),     lds64<N>(v1),
+                                    lds64<H>(v0), lds64<H>(v1), lds64<H + N>(v0), lds64<H + N>(v1)};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    vw[k][0] = x[k].x; vw[k][1] = x[k].y;
+                for (int k = 0; k < 8; ++k) {
+                    vw[k >> 2][k & 3][0] = x[k].x; vw[k >> 2][k & 3][1] = x[k].y;
                 }
             }
         }
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-            unsigned a[2][4];  // [tokens 2t, 2t + 1 | 2t + 8, 2t + 9][code of the word]
-            q8_v_halves<FMT>(vw[0][i], vw[1][i], a[0]);
-            q8_v_halves<FMT>(vw[2][i], vw[3][i], a[1]);
+            unsigned a[2][2][4];  // [half][tokens 2t, 2t + 1 | 2t + 8, 2t + 9][code of the word]
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                q8_v_halves<FMT>(vw[j][0][i], vw[j][1][i], a[j][0]);
+                q8_v_halves<FMT>(vw[j][2][i], vw[j][3][i], a[j][1]);
+            }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 // a tile's products start from zero and are added in fp32: the
                 // tensor core truncates its sums, which over the hundreds of
                 // tiles of a long request would cost 4e-6 of the output
                 float d[4];
-                q8_mma0(d, a[0][2 * k], a[0][2 * k + 1], a[1][2 * k], a[1][2 * k + 1], b[0][0], b[0][1]);
-                if constexpr (SPLIT)
-                    q8_mma(d, a[0][2 * k], a[0][2 * k + 1], a[1][2 * k], a[1][2 * k + 1], b[1][0], b[1][1]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int y = 0; y < (SPLIT ? 2 : 1); ++y) {
+                        if (j == 0 && y == 0)
+                            q8_mma0(d, a[j][0][2 * k], a[j][0][2 * k + 1], a[j][1][2 * k], a[j][1][2 * k + 1], b[j][y][0],
+                                    b[j][y][1]);
+                        else
+                            q8_mma(d, a[j][0][2 * k], a[j][0][2 * k + 1], a[j][1][2 * k], a[j][1][2 * k + 1], b[j][y][0],
+                                   b[j][y][1]);
+                    }
                 o[2 * i + k][0] = add2(o[2 * i + k][0], pack2(d[0], d[1]));
                 o[2 * i + k][1] = add2(o[2 * i + k][1], pack2(d[2], d[3]));
             }

@@ -2,12 +2,12 @@
 // sm_100a (ckv_dense_decode_q8): the dense comparator of ckv_decode.cu for this
 // cache.  The tile arithmetic and what bounds it: ckv_q8_attend.cuh.
 //
-// Work split: every (request, KV head) is a unit of ceil(len/16) tiles; each
+// Work split: every (request, KV head) is a unit of ceil(len/32) tiles; each
 // block has one range of tiles, found by every block for itself from the lengths.
 // Where pieces of about an equal share that do not cross units are no more than
 // the blocks, each block has one piece, and so one start and one join; otherwise
 // the units are laid end to end and cut into equal ranges, which may cross units.
-// The second way costs a block that crosses a unit about 16 tiles' time (a new
+// The second way costs a block that crosses a unit about 12 tiles' time (a new
 // query, an empty ring, a join), the first the difference between the longest
 // piece and the share: the smaller loss decides.  (Finer pieces by ticket, for the
 // SMs' 10 % difference in bandwidth, lost more by their starts: 8 requests of
@@ -23,17 +23,16 @@
 
 namespace ckv {
 
-constexpr int QD_WARPS = 4;
+constexpr int QD_WARPS = 6;
 constexpr int QD_THREADS = QD_WARPS * 32;
-constexpr int QD_CTAS = 4;          // resident blocks per SM
-constexpr int QD_MAX_GRID = 640;    // >= QD_CTAS * SMs
-constexpr int QD_MIN_PIECE = 16;    // tiles: below it more partials cost more than they save
-constexpr int QD_CROSS = 16;        // tiles: what crossing a unit costs a block
-constexpr int QD_LANES = 32;        // tiles per index window
+constexpr int QD_CTAS = 2;          // resident blocks per SM
+constexpr int QD_MAX_GRID = 320;    // >= QD_CTAS * SMs
+constexpr int QD_MIN_PIECE = 24;    // tiles: below it more partials cost more than they save
+constexpr int QD_CROSS = 12;        // tiles: what crossing a unit costs a block
 
 template <int D>
 struct QdStages {
-    static constexpr int v = D == 128 ? 3 : 5;  // 16 warps x 2 (4) tiles ahead: at least 64 KB in flight per SM
+    static constexpr int v = D == 128 ? 2 : 4;  // 12 warps x 1 (3) tiles ahead: 96 KB in flight per SM
 };
 
 struct DenseQ8Params {
@@ -72,8 +71,8 @@ __device__ __forceinline__ void join_partials(const DenseQ8Params& p, int c0, in
                                               unsigned char* smem, float* s_head, int tid) {
     constexpr int JOIN = DenseQ8Smem<D, GQ>::JOIN;
     constexpr int VECS = GQ * D / 4;  // float4 of an output
-    constexpr int SHARE = QD_THREADS / VECS > 0 ? QD_THREADS / VECS : 1;
-    constexpr int PER = VECS > QD_THREADS ? VECS / QD_THREADS : 1;
+    constexpr int SHARE = QD_THREADS / VECS > 0 ? QD_THREADS / VECS : 1;      // threads to a float4
+    constexpr int PER = SHARE > 1 ? 1 : (VECS + QD_THREADS - 1) / QD_THREADS;  // float4 to a thread
     const int lane = tid & 31, warp = tid >> 5;
     float* s_f = reinterpret_cast<float*>(smem);  // [JOIN][GQ] references, then weights
     float* s_l = s_f + JOIN * GQ;                 // [JOIN][GQ] sums
@@ -85,7 +84,7 @@ __device__ __forceinline__ void join_partials(const DenseQ8Params& p, int c0, in
         s_m[tid] = Q8_M_INIT;
         s_sum[tid] = 0.f;
     }
-    const int part = tid / VECS;
+    const int part = SHARE > 1 ? tid / VECS : 0, x0 = SHARE > 1 ? tid % VECS : tid;
     float4 A[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) A[k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -122,14 +121,15 @@ __device__ __forceinline__ void join_partials(const DenseQ8Params& p, int c0, in
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
-            const int x = tid % VECS + k * QD_THREADS, h = x / (D / 4);
+            const int x = x0 + k * QD_THREADS, h = x / (D / 4);
+            if (x >= VECS || part >= SHARE) continue;
             const float4* acc = reinterpret_cast<const float4*>(p.acc) + x;
             const float fo = s_old[h];
             A[k].x *= fo;
             A[k].y *= fo;
             A[k].z *= fo;
             A[k].w *= fo;
-#pragma unroll 8
+#pragma unroll 16
             for (int i = part; i < n; i += SHARE) {
                 const float4 v = __ldcg(acc + (size_t)slot_of(i) * VECS);
                 const float f = s_f[i * GQ + h];
@@ -157,7 +157,8 @@ __device__ __forceinline__ void join_partials(const DenseQ8Params& p, int c0, in
     if (part == 0) {
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
-            const int x = tid + k * QD_THREADS;
+            const int x = x0 + k * QD_THREADS;
+            if (x >= VECS) continue;
             const float L = s_sum[x / (D / 4)];
             const float inv = L == 0.f ? 0.f : 1.f / L;  // no weight: every block of the unit was out of range
             reinterpret_cast<float4*>(out)[x] = make_float4(A[k].x * inv, A[k].y * inv, A[k].z * inv, A[k].w * inv);
@@ -165,25 +166,25 @@ __device__ __forceinline__ void join_partials(const DenseQ8Params& p, int c0, in
     }
 }
 
-// A whole tile, K and V, each 16 D contiguous bytes (k, v: lane's first 16 of them).
-// Rows 4 apart (d = 128) or 8 apart (d = 64) differ in the swizzle by one bit, or none.
-template <int D>
-__device__ __forceinline__ void copy_tile(unsigned sm, const char* k, const char* v, int lane) {
-    constexpr int TILE = Q8Geom<D>::TILE;
+// 16 whole rows of K and of V, each 16 D contiguous bytes (k, v: lane's first 16 of
+// them), to sm + SO.  Rows 4 apart (d = 128) differ in the swizzle by one bit.
+template <int D, int SO>
+__device__ __forceinline__ void copy_half(unsigned sm, const char* k, const char* v, int lane) {
+    constexpr int V = Q8Geom<D>::V + SO;
     const unsigned even = sm + q8_swz<D>(lane / Q8Geom<D>::CH, lane % Q8Geom<D>::CH);
-    cp_async_16i<0, 0>(even, k);
-    cp_async_16i<TILE, 0>(even, v);
+    cp_async_16i<SO, 0>(even, k);
+    cp_async_16i<V, 0>(even, v);
     if constexpr (D == 128) {
         const unsigned odd = sm + (q8_swz<D>(lane / 8, lane % 8) ^ 64);
-        cp_async_16i<512, 512>(odd, k);
-        cp_async_16i<1024, 1024>(even, k);
-        cp_async_16i<1536, 1536>(odd, k);
-        cp_async_16i<TILE + 512, 512>(odd, v);
-        cp_async_16i<TILE + 1024, 1024>(even, v);
-        cp_async_16i<TILE + 1536, 1536>(odd, v);
+        cp_async_16i<SO + 512, 512>(odd, k);
+        cp_async_16i<SO + 1024, 1024>(even, k);
+        cp_async_16i<SO + 1536, 1536>(odd, k);
+        cp_async_16i<V + 512, 512>(odd, v);
+        cp_async_16i<V + 1024, 1024>(even, v);
+        cp_async_16i<V + 1536, 1536>(odd, v);
     } else {
-        cp_async_16i<512, 512>(even, k);
-        cp_async_16i<TILE + 512, 512>(even, v);
+        cp_async_16i<SO + 512, 512>(even, k);
+        cp_async_16i<V + 512, 512>(even, v);
     }
 }
 
@@ -193,7 +194,6 @@ __global__ void __launch_bounds__(QD_THREADS, QD_CTAS) dense_q8_kernel(const __g
     using SM = DenseQ8Smem<D, GQ>;
     constexpr int STAGES = QdStages<D>::v;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ int s_scan[33];
     __shared__ int s_last;
     const TableView& t = p.c.t;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -201,32 +201,24 @@ __global__ void __launch_bounds__(QD_THREADS, QD_CTAS) dense_q8_kernel(const __g
     unsigned char* ring = smem + warp * SM::WARP;
     float* wm = reinterpret_cast<float*>(smem + QD_WARPS * SM::WARP);  // [warps][GQ]
     float* wl = wm + QD_WARPS * GQ;
-    int* s_nt = reinterpret_cast<int*>(smem + SM::FIXED);              // B > 32: [B] tiles of a unit of request b
-    int* s_pre = s_nt + B;                                             // [B] positions or items before request b
+    int* s_nt = reinterpret_cast<int*>(smem + SM::FIXED);              // [B] tiles of a unit of request b
     pdl_wait();
 
-    auto tiles_of = [&](int b) {
+    for (int b = tid; b < B; b += QD_THREADS) {
         const int n = t.len[b];
-        if (n >= 0 && n <= (long long)t.max_blocks * bs) return (n + Q8_TOK - 1) / Q8_TOK;
-        if (blockIdx.x == 0) atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
-        return 0;
-    };
-    auto ceil_div = [](int a, int b) { return (int)(((unsigned)a + b - 1) / (unsigned)b); };
-    // Up to 32 requests every warp works with one a lane, without a block barrier;
-    // more are shared out over the threads.
-    const bool small = B <= 32;
-    const int seg = ceil_div(B, QD_THREADS);
-    const int b0 = min(B, tid * seg), b1 = min(B, b0 + seg);
-    int my_nt = 0, my_pre = 0, all = 0;
-    if (small) {
-        my_nt = lane < B ? tiles_of(lane) : 0;
-        all = __reduce_add_sync(FULL, my_nt);
-    } else {
-        int own = 0;
-        for (int b = b0; b < b1; ++b) own += s_nt[b] = tiles_of(b);
-        block_exclusive_scan(own, s_scan, &all);
+        const bool ok = n >= 0 && n <= (long long)t.max_blocks * bs;
+        if (!ok && blockIdx.x == 0) atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
+        s_nt[b] = ok ? (n + Q8_TOK - 1) / Q8_TOK : 0;
     }
-    const int total = all * Hkv;
+    __syncthreads();
+    // from here every warp works for itself, 32 requests at a time
+    auto ceil_div = [](int a, int b) { return (int)(((unsigned)a + b - 1) / (unsigned)b); };
+    auto sum_over = [&](auto f) {
+        int own = 0;
+        for (int b = lane; b < B; b += 32) own += f(s_nt[b]);
+        return __reduce_add_sync(FULL, own);
+    };
+    const int total = sum_over([](int nt) { return nt; }) * Hkv;
     if (total == 0) {
         for (int i = blockIdx.x * QD_THREADS + tid; i < B * p.c.Hq * D; i += grid * QD_THREADS) p.out[i] = 0.f;
         return;
@@ -235,71 +227,45 @@ __global__ void __launch_bounds__(QD_THREADS, QD_CTAS) dense_q8_kernel(const __g
     // pieces of at most `piece` tiles: 0 where the units are laid end to end instead
     const int per = max(share, QD_MIN_PIECE);
     const int most = per + max(QD_CROSS, share >> 4);
-    const int step = max(1, (most - per) / (small ? 8 : 3));
     int piece = per, items = 0;
     while (true) {
-        int own = 0;
-        if (small) {
-            own = __reduce_add_sync(FULL, ceil_div(my_nt, piece));
-        } else {
-            int mine = 0;
-            for (int b = b0; b < b1; ++b) mine += ceil_div(s_nt[b], piece);
-            block_exclusive_scan(mine, s_scan, &own);
-        }
-        items = own * Hkv;
+        items = sum_over([&](int nt) { return ceil_div(nt, piece); }) * Hkv;
         if (items <= grid) break;
-        if (piece >= most) {
+        if (piece >= most || B * Hkv > 2 * grid) {
             piece = 0;
             break;
         }
-        piece = min(piece + step, most);
+        piece = min(piece + max(1, (most - per) >> 2), most);
     }
-    // [start, end): this block's range, in pieces or in tiles, and what comes before each request
+    // [start, end): this block's range, in pieces or in tiles
     const int start = piece ? (int)blockIdx.x : (int)min((long long)blockIdx.x * per, (long long)total);
     const int end = piece ? min(start + 1, items) : min(start + per, total);
-    if (small) {
-        const int own = piece ? ceil_div(my_nt, piece) : my_nt;
-        my_pre = own;
-#pragma unroll
-        for (int k = 1; k < 32; k <<= 1) {
-            const int y = __shfl_up_sync(FULL, my_pre, k);
-            if (lane >= k) my_pre += y;
-        }
-        my_pre = (my_pre - own) * Hkv;
-    } else {
-        int own = 0, none;
-        for (int b = b0; b < b1; ++b) own += piece ? ceil_div(s_nt[b], piece) : s_nt[b];
-        int run = block_exclusive_scan(own, s_scan, &none);
-        for (int b = b0; b < b1; ++b) {
-            s_pre[b] = run * Hkv;
-            run += piece ? ceil_div(s_nt[b], piece) : s_nt[b];
-        }
-        __syncthreads();
-    }
     for (int b = blockIdx.x; b < B; b += grid)
-        if ((small ? __shfl_sync(FULL, my_nt, b & 31) : s_nt[b]) == 0)  // nothing to attend to
+        if (s_nt[b] == 0)  // nothing to attend to
             for (int i = tid; i < p.c.Hq * D; i += QD_THREADS) p.out[(size_t)b * p.c.Hq * D + i] = 0.f;
 
     Q8Warp<D, GQ, FMT> st;
     for (int at = start; at < end;) {
         // the segment: tiles [lo, hi) of KV head h of request b, the unit shared by the blocks c0 .. c0 + np - 1
-        int b, nt, pre;
-        if (small) {
-            b = 31 - __clz(__ballot_sync(FULL, lane < B && my_nt > 0 && my_pre <= at));
-            nt = __shfl_sync(FULL, my_nt, b);
-            pre = __shfl_sync(FULL, my_pre, b);
-        } else {
-            int hi = B;
-            b = 0;
-            while (hi - b > 1) {
-                const int mid = (b + hi) >> 1;
-                if (s_pre[mid] <= at) b = mid;
-                else hi = mid;
+        int b = 0, pre = 0;  // pre: what comes before request b
+        for (int k = 0;; k += 32) {
+            const int x = k + lane < B ? s_nt[k + lane] : 0;
+            int own = (piece ? ceil_div(x, piece) : x) * Hkv, inc = own;
+#pragma unroll
+            for (int y = 1; y < 32; y <<= 1) {
+                const int z = __shfl_up_sync(FULL, inc, y);
+                if (lane >= y) inc += z;
             }
-            while (s_nt[b] == 0) --b;  // empty requests share their place with the one before
-            nt = s_nt[b];
-            pre = s_pre[b];
+            const int chunk = __shfl_sync(FULL, inc, 31);
+            if (at < pre + chunk) {  // the first request that ends past `at`
+                const int l = __ffs(__ballot_sync(FULL, at < pre + inc)) - 1;
+                b = k + l;
+                pre += __shfl_sync(FULL, inc - own, l);
+                break;
+            }
+            pre += chunk;
         }
+        const int nt = s_nt[b];
         int h, lo, hi, c0, np, odd = 0, slot = 2 * blockIdx.x;
         if (piece) {
             np = ceil_div(nt, piece);
@@ -326,46 +292,59 @@ __global__ void __launch_bounds__(QD_THREADS, QD_CTAS) dense_q8_kernel(const __g
         const int32_t* table = t.table + (size_t)b * t.max_blocks;
 
         const int nit = (hi - lo - warp + QD_WARPS - 1) / QD_WARPS;  // this warp's tiles: lo + warp + QD_WARPS i
+        // a window of 16 tiles: lane 2 i + j holds the block of half j of this warp's tile i
         auto block_of = [&](int x) {
-            const int tile = lo + warp + QD_WARPS * x;
-            return x < nit ? table[(tile * Q8_TOK) >> t.sh] : 0;
+            const int pos = (lo + warp + QD_WARPS * (x + (lane >> 1))) * Q8_TOK + (lane & 1) * Q8_HALF;
+            return x + (lane >> 1) < nit && pos < n ? table[pos >> t.sh] : 0;
         };
-        int win_cur = block_of(lane), win_nxt = block_of(QD_LANES + lane);
+        int win_cur = block_of(0), win_nxt = block_of(16);
         const unsigned ring32 = smem_addr32(ring);
         const char* klane = static_cast<const char*>(p.c.k) + lane * 16;
         const char* vlane = static_cast<const char*>(p.c.v) + lane * 16;
-        const float* slane = lane == 0 ? p.c.k_scale : p.c.v_scale;  // lanes 0 and 1 copy the scales
+        const float* slane = lane < 2 ? p.c.k_scale : p.c.v_scale;  // lanes 0..3 copy the halves' scales
         unsigned stage_in = 0;
-        unsigned bad = 0;  // staged tiles, by ring slot, whose block is out of range
+        unsigned bad = 0;  // bit 2 s + j: the block of half j of the tile in ring slot s is out of range
         auto issue = [&](int x) {
             if (x < nit) {
-                if ((x & (QD_LANES - 1)) == 0 && x > 0) {
+                if ((x & 15) == 0 && x > 0) {
                     win_cur = win_nxt;
-                    win_nxt = block_of(x + QD_LANES + lane);
+                    win_nxt = block_of(x + 16);
                 }
                 const unsigned sm = ring32 + stage_in * QG::SLOT;
-                const int id = __shfl_sync(FULL, win_cur, x & (QD_LANES - 1));
+                const int id0 = __shfl_sync(FULL, win_cur, 2 * (x & 15)), id1 = __shfl_sync(FULL, win_cur, 2 * (x & 15) + 1);
                 const int pos = (lo + warp + QD_WARPS * x) * Q8_TOK;
-                bad &= ~(1u << stage_in);
-                if ((unsigned)id < (unsigned)t.n_blocks) {
-                    const unsigned unit = id * Hkv + h;
-                    const size_t src = (size_t)((unit << t.sh) + (pos & (bs - 1))) * D;
-                    if (pos + Q8_TOK <= n) {
-                        copy_tile<D>(sm, klane + src, vlane + src, lane);
-                    } else {
-#pragma unroll
-                        for (int y = 0; y < QG::TILE / 512; ++y) {
-                            const int idx = y * 32 + lane, row = idx / QG::CH, c = idx % QG::CH;
-                            const unsigned dst = sm + q8_swz<D>(row, c);
-                            const int size = pos + row < n ? 16 : 0;
-                            cp_async_16s(dst, klane + src + y * 512, size);
-                            cp_async_16s(dst + QG::TILE, vlane + src + y * 512, size);
-                        }
-                    }
-                    cp_async_4p(sm + QG::SCALES + lane * 64, slane + unit, lane < 2);
+                const bool ok0 = (unsigned)id0 < (unsigned)t.n_blocks, ok1 = (unsigned)id1 < (unsigned)t.n_blocks;
+                const unsigned unit0 = id0 * Hkv + h, unit1 = id1 * Hkv + h;
+                const size_t src0 = (size_t)((unit0 << t.sh) + (pos & (bs - 1))) * D;
+                const size_t src1 = (size_t)((unit1 << t.sh) + ((pos + Q8_HALF) & (bs - 1))) * D;
+                if (pos + Q8_TOK <= n && ok0 && ok1) {
+                    copy_half<D, 0>(sm, klane + src0, vlane + src0, lane);
+                    copy_half<D, QG::HALF>(sm, klane + src1, vlane + src1, lane);
+                    bad &= ~(3u << 2 * stage_in);
+                    cp_async_4p(sm + QG::SCALES + lane * 64, slane + (lane & 1 ? unit1 : unit0), lane < 4);
                 } else {
-                    bad |= 1u << stage_in;
-                    if (lane == 0) atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
+                    // the end of the request, or a block out of range: zeros where there is nothing
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const bool ok = j ? ok1 : ok0;
+                        const size_t src = ok ? (j ? src1 : src0) : 0;
+                        const int rows = ok ? n - pos - j * Q8_HALF : 0;
+#pragma unroll
+                        for (int y = 0; y < QG::HALF / 512; ++y) {
+                            const int idx = y * 32 + lane, row = idx / QG::CH, c = idx % QG::CH;
+                            const unsigned dst = sm + j * QG::HALF + q8_swz<D>(row, c);
+                            const int size = row < rows ? 16 : 0;
+                            const size_t from = size ? src + y * 512 : 0;
+                            cp_async_16s(dst, klane + from, size);
+                            cp_async_16s(dst + QG::V, vlane + from, size);
+                        }
+                        if (lane < 2)
+                            cp_async_4s(sm + QG::SCALES + 64 * j + 128 * lane,
+                                        (lane ? p.c.v_scale : p.c.k_scale) + (rows > 0 ? (j ? unit1 : unit0) : 0),
+                                        rows > 0 ? 4 : 0);
+                    }
+                    bad = (bad & ~(3u << 2 * stage_in)) | ((ok0 ? 0u : 1u) | (ok1 ? 0u : 2u)) << 2 * stage_in;
+                    if (lane == 0 && !(ok0 && ok1)) atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
                 }
             }
             stage_in = stage_in + 1 == STAGES ? 0 : stage_in + 1;
@@ -382,7 +361,9 @@ __global__ void __launch_bounds__(QD_THREADS, QD_CTAS) dense_q8_kernel(const __g
             issue(x + STAGES - 1);
             cp_async_wait<STAGES - 1>();
             __syncwarp();  // what the other lanes copied is visible
-            const unsigned mask = bad >> stage_out & 1u ? 0u : left >= Q8_TOK ? 0xffffu : 0xffffu >> (Q8_TOK - left);
+            unsigned mask = 0xffffffffu;
+            if (left < Q8_TOK) mask >>= Q8_TOK - left;
+            if (bad) mask &= ~((bad >> 2 * stage_out & 1u) * 0xffffu | (bad >> 2 * stage_out & 2u) * 0x7fff8000u);
             st.template tile<true, false>(ring32 + stage_out * QG::SLOT, mask, lane, [](int, float) {});
             left -= QD_WARPS * Q8_TOK;
             stage_out = stage_out + 1 == STAGES ? 0 : stage_out + 1;
@@ -437,12 +418,12 @@ template <int D, int GQ, int FMT>
 static cudaError_t launch_dense_q8_t(const DenseQ8Params& p, cudaStream_t st) {
     static LaunchCache lc;
     auto kern = dense_q8_kernel<D, GQ, FMT>;
-    const size_t smem = DenseQ8Smem<D, GQ>::FIXED + 2 * (size_t)p.c.t.B * 4;
+    const size_t smem = DenseQ8Smem<D, GQ>::FIXED + (size_t)p.c.t.B * 4;
     int per_sm = 0, sms = 0;
     cudaError_t e = prepare_launch(kern, lc, smem, QD_THREADS, &per_sm, &sms);
     if (e != cudaSuccess) return e;
     if (sms <= 0 || per_sm <= 0) return cudaErrorInvalidConfiguration;
-    const long long tiles = (long long)p.c.t.B * p.c.Hkv * p.c.t.max_blocks * (p.c.t.block / Q8_TOK);
+    const long long tiles = (long long)p.c.t.B * p.c.Hkv * p.c.t.max_blocks * p.c.t.block / Q8_TOK + (long long)p.c.t.B * p.c.Hkv;
     const int grid = (int)min((long long)min(sms * per_sm, QD_MAX_GRID), (tiles + QD_MIN_PIECE - 1) / QD_MIN_PIECE);
     return launch_pdl(KK_ATTENTION, kern, dim3(grid), dim3(QD_THREADS), smem, st, p);
 }

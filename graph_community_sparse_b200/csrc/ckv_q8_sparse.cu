@@ -16,8 +16,8 @@
 namespace ckv {
 
 constexpr int QS_WARPS = 4;
-constexpr int QS_STAGES = 3;
-constexpr int QS_CTAS = 4;  // resident blocks per SM
+constexpr int QS_STAGES = 2;
+constexpr int QS_CTAS = 3;  // resident blocks per SM
 
 struct SparseQ8Params {
     DecodeParams d;
@@ -39,48 +39,42 @@ __device__ __forceinline__ void sparse_q8_segment(const SparseQ8Params& p, int u
     const auto raw_q = Q8Warp<D, GQ, FMT>::fetch_q(
         Q8Warp<D, GQ, FMT>::q_row(p.d.q, p.c.dtype, (size_t)b * p.d.Hq + h0), p.c.dtype, lane);
 
-    // windows of 32 list entries (two tiles): positions two windows ahead of the
-    // copies, pool rows (-1: not attended) one window ahead
-    auto positions = [&](int w) { return w * 32 + lane < n ? toks[lo + w * 32 + lane] : -1; };
-    auto rows = [&](int pos, int w) {
+    // a tile's 32 list entries, one a lane: positions two tiles ahead of the
+    // copies, pool rows (-1: not attended) one tile ahead
+    auto positions = [&](int i) { return i * Q8_TOK + lane < n ? toks[lo + i * Q8_TOK + lane] : -1; };
+    auto rows = [&](int pos, int i) {
         int row = -1;
         if ((unsigned)pos < (unsigned)max(len, 0)) {
             const int id = table[pos >> t.sh];
             if ((unsigned)id < (unsigned)t.n_blocks) row = ((id * p.c.Hkv + kvh) << t.sh) + (pos & (t.block - 1));
         }
-        if (row < 0 && w * 32 + lane < n) atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
+        if (row < 0 && i * Q8_TOK + lane < n) atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
         return row;
     };
-    int row_cur = rows(positions(0), 0);
     int pos_nxt = positions(1);
-    int row_nxt = rows(pos_nxt, 1);
-    pos_nxt = positions(2);
+    int row_nxt = rows(positions(0), 0);
     int stage_in = 0;
     auto issue = [&](int i) {
         if (i < nit) {
-            if (i > 0 && (i & 1) == 0) {
-                const int w = i >> 1;
-                row_cur = row_nxt;
-                row_nxt = rows(pos_nxt, w + 1);
-                pos_nxt = positions(w + 2);
-            }
+            const int row_cur = row_nxt;
+            row_nxt = rows(pos_nxt, i + 1);
+            pos_nxt = positions(i + 2);
             unsigned char* slot_p = ring + stage_in * QG::SLOT;
             const unsigned sm = smem_addr32(slot_p);
-            const int base = (i & 1) << 4;
 #pragma unroll
-            for (int x = 0; x < QG::TILE / 512; ++x) {
+            for (int x = 0; x < 2 * QG::HALF / 512; ++x) {
                 const int idx = x * 32 + lane, r = idx / QG::CH, c = idx % QG::CH;
-                const int row = __shfl_sync(FULL, row_cur, base + r);
+                const int row = __shfl_sync(FULL, row_cur, r);
                 const int size = row >= 0 ? 16 : 0;
                 const size_t src = (size_t)max(row, 0) * D + c * 16;
-                const unsigned dst = sm + q8_swz<D>(r, c);
+                const unsigned dst = sm + (r >> 4) * QG::HALF + q8_swz<D>(r & 15, c);
                 cp_async_16s(dst, static_cast<const char*>(p.c.k) + src, size);
-                cp_async_16s(dst + QG::TILE, static_cast<const char*>(p.c.v) + src, size);
+                cp_async_16s(dst + QG::V, static_cast<const char*>(p.c.v) + src, size);
             }
-            const int row = __shfl_sync(FULL, row_cur, base + (lane & 15));
-            cp_async_4s(sm + QG::SCALES + lane * 4, (lane < 16 ? p.c.k_scale : p.c.v_scale) + (max(row, 0) >> t.sh),
-                        row >= 0 ? 4 : 0);
-            const unsigned mask = __ballot_sync(FULL, row >= 0) & 0xffffu;
+            const int unit = max(row_cur, 0) >> t.sh, size = row_cur >= 0 ? 4 : 0;
+            cp_async_4s(sm + QG::SCALES + lane * 4, p.c.k_scale + unit, size);
+            cp_async_4s(sm + QG::SCALES + 128 + lane * 4, p.c.v_scale + unit, size);
+            const unsigned mask = __ballot_sync(FULL, row_cur >= 0);
             if (lane == 0) *reinterpret_cast<unsigned*>(slot_p + QG::MASK) = mask;
         }
         stage_in = stage_in + 1 == QS_STAGES ? 0 : stage_in + 1;
@@ -103,7 +97,7 @@ __device__ __forceinline__ void sparse_q8_segment(const SparseQ8Params& p, int u
             const unsigned mask = *reinterpret_cast<const unsigned*>(sm + QG::MASK);
             if constexpr (decltype(nbr)::value) {
                 // an all-invalid tile has no logits of its own to store
-                if (mask == 0u && lane < 16 && i * Q8_TOK + lane < n) lamu[i * Q8_TOK + lane] = -INFINITY;
+                if (mask == 0u && i * Q8_TOK + lane < n) lamu[i * Q8_TOK + lane] = -INFINITY;
             }
             st.template tile<false, decltype(nbr)::value>(smem_addr32(sm), mask, lane, [&](int k, float x) {
                 if (i * Q8_TOK + k < n) lamu[i * Q8_TOK + k] = x;
