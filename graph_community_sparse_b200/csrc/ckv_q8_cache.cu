@@ -8,34 +8,37 @@
 namespace ckv {
 
 // ---------------------------------------------------------------------------
-// block-wide exclusive scan of one 64-bit integer per thread
+// block-wide exclusive scan of N 64-bit integers per thread, their totals in
+// total; one barrier, and s_warp ([N][32]) must not be in use still
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ long long block_exclusive_scan64(long long x, long long* s_warp, long long* total) {
+template <int N>
+__device__ __forceinline__ void block_exclusive_scan64(long long (&x)[N], long long* s_warp, long long (&total)[N]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    long long inc = x;
+    long long inc[N];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(FULL, inc, o);
-        if (lane >= o) inc += y;
+    for (int i = 0; i < N; ++i) {
+        inc[i] = x[i];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(FULL, inc[i], o);
+            if (lane >= o) inc[i] += y;
+        }
+        if (lane == 31) s_warp[i * 32 + warp] = inc[i];
     }
-    if (lane == 31) s_warp[warp] = inc;
     __syncthreads();
-    if (warp == 0) {
-        const long long w = lane < nw ? s_warp[lane] : 0;
+    // every warp scans the warps' totals for itself
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const long long w = lane < nw ? s_warp[i * 32 + lane] : 0;
         long long wi = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(FULL, wi, o);
             if (lane >= o) wi += y;
         }
-        if (lane < nw) s_warp[lane] = wi - w;
-        if (lane == 31) s_warp[32] = wi;
+        total[i] = __shfl_sync(FULL, wi, 31);
+        x[i] = __shfl_sync(FULL, wi - w, warp) + inc[i] - x[i];
     }
-    __syncthreads();
-    const long long r = s_warp[warp] + inc - x;
-    *total = s_warp[32];
-    __syncthreads();
-    return r;
 }
 
 // Largest i in [0, n) with a[i] <= x, given a[0] <= x (a ascending).
@@ -57,13 +60,14 @@ __device__ __forceinline__ int last_le(const int* a, int n, int x) {
 // shares the writes.  A cluster barrier separates what is read from the state
 // from what is written to it, and the blocks given back from those taken.
 // ---------------------------------------------------------------------------
-constexpr int PLAN_THREADS = 512;
+constexpr int PLAN_THREADS = 1024;
 constexpr int PLAN_CLUSTER = 8;
 
 struct PlanParams {
     TableView t;
     PlanView p;
     const int32_t* add;
+    int rows_here;  // rows whose slots the plan kernel writes itself
 };
 
 __device__ __forceinline__ void cluster_sync() {
@@ -72,9 +76,9 @@ __device__ __forceinline__ void cluster_sync() {
 
 __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constant__ PlanParams q) {
     extern __shared__ int s_plan[];
-    __shared__ long long s_warp[33];
+    __shared__ long long s_warp[128];
     const TableView& t = q.t;
-    const int B = t.B, bs = t.block, sh = t.sh, W = t.max_blocks;
+    const int B = t.B, bs = t.block, sh = t.sh, W = t.max_blocks, threads = blockDim.x;
     int* s_n1 = s_plan;             // [B] tokens after the drops
     int* s_n2 = s_n1 + B;           // [B] tokens after the growth
     int* s_gone = s_n2 + B;         // [B + 1] blocks given back before request b
@@ -82,15 +86,15 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
     int* s_start = s_need + B + 1;  // [B + 1] first row of request b
     pdl_wait();
     const int tid = threadIdx.x;
-    const int gthreads = gridDim.x * PLAN_THREADS, gtid = blockIdx.x * PLAN_THREADS + tid;
+    const int gthreads = gridDim.x * threads, gtid = blockIdx.x * threads + tid;
     const int n_free = max(0, min(*t.n_free, t.n_blocks));
     const long long cap = (long long)W << sh;
     auto blocks = [&](int n) { return (int)(((long long)n + bs - 1) >> sh); };
 
     // drops, and the rows asked for.  Thread i handles requests [b0, b1).
-    const int seg = (B + PLAN_THREADS - 1) / PLAN_THREADS;
+    const int seg = (B + threads - 1) / threads;
     const int b0 = min(B, tid * seg), b1 = min(B, b0 + seg);
-    long long gone = 0, up = 0;
+    long long gu[2] = {0, 0};  // blocks given back, rows asked for
     for (int b = b0; b < b1; ++b) {
         const int n0 = t.len[b], a = q.add[b];
         const bool bad = n0 < 0 || n0 > cap;
@@ -98,17 +102,18 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
         const int n1 = bad ? 0 : a < 0 ? (int)max(0ll, (long long)n0 + a) : n0;
         s_n1[b] = n1;
         s_gone[b] = bad ? 0 : blocks(n0) - blocks(n1);
-        gone += s_gone[b];
-        up += max(a, 0);
+        gu[0] += s_gone[b];
+        gu[1] += max(a, 0);
     }
-    long long total_up, total_gone, total_need;
-    long long run_up = block_exclusive_scan64(up, s_warp, &total_up);
-    long long run_gone = block_exclusive_scan64(gone, s_warp, &total_gone);
+    long long totals[2];
+    block_exclusive_scan64<2>(gu, s_warp, totals);
+    long long run_gone = gu[0], run_up = gu[1];
+    const long long total_gone = totals[0], total_up = totals[1];
     const int freed = (int)min(total_gone, (long long)t.n_blocks - n_free);  // less only when the state is corrupt
     const int avail = n_free + freed;
 
     // growth that fits the table and the slot map, and the blocks it needs
-    long long need = 0;
+    long long need[1] = {0}, need_all[1];
     for (int b = b0; b < b1; ++b) {
         const int a = max(q.add[b], 0), n0 = t.len[b];
         const bool bad = n0 < 0 || n0 > cap;
@@ -121,9 +126,11 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
         s_n2[b] = fits ? s_n1[b] + a : -1;
         const int x = fits ? blocks(s_n2[b]) - blocks(s_n1[b]) : 0;
         s_need[b] = x;
-        need += x;
+        need[0] += x;
     }
-    long long run_need = block_exclusive_scan64(need, s_warp, &total_need);
+    block_exclusive_scan64<1>(need, s_warp + 64, need_all);
+    long long run_need = need[0];
+    const long long total_need = need_all[0];
     for (int b = b0; b < b1; ++b) {
         const int x = s_need[b];
         s_need[b] = (int)min(run_need, (long long)avail);
@@ -141,12 +148,25 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
     }
     __syncthreads();
 
-    // blocks given back: the k-th of them at free_list[avail - 1 - k]
-    for (int k = gtid; k < freed; k += gthreads) {
-        const int b = last_le(s_gone, B + 1, k);
-        const size_t at = (size_t)b * W + blocks(s_n1[b]) + (k - s_gone[b]);
-        t.free_list[avail - 1 - k] = t.table[at];
-        t.table[at] = -1;
+    // blocks given back: the k-th of them at free_list[avail - 1 - k].  A thread
+    // takes 4 consecutive ones: one search, the loads independent of each other.
+    for (int k0 = gtid * 4; k0 < freed; k0 += gthreads * 4) {
+        int b = last_le(s_gone, B + 1, k0);
+        size_t at[4];
+        int id[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = min(k0 + i, freed - 1);
+            while (k >= s_gone[b + 1]) ++b;
+            at[i] = (size_t)b * W + blocks(s_n1[b]) + (k - s_gone[b]);
+            id[i] = t.table[at[i]];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (k0 + i >= freed) break;
+            t.free_list[avail - 1 - (k0 + i)] = id[i];
+            t.table[at[i]] = -1;
+        }
     }
     // everybody has read len, add and n_free and given blocks back
     if (gridDim.x > 1) cluster_sync();
@@ -156,34 +176,38 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
     // range of k is empty or belongs to nobody (all needs after the first
     // refusal for want of blocks are refused).
     const int taken = s_need[B];
-    for (int k = gtid; k < taken; k += gthreads) {
-        const int b = last_le(s_need, B + 1, k);
-        const int j = blocks(s_n1[b]) + (k - s_need[b]);
-        if (j < blocks(s_n2[b])) t.table[(size_t)b * W + j] = __ldcg(t.free_list + avail - 1 - k);
+    for (int k0 = gtid * 4; k0 < taken; k0 += gthreads * 4) {
+        int b = last_le(s_need, B + 1, k0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = k0 + i;
+            if (k >= taken) break;
+            while (k >= s_need[b + 1]) ++b;
+            const int j = blocks(s_n1[b]) + (k - s_need[b]);
+            if (j < blocks(s_n2[b])) t.table[(size_t)b * W + j] = __ldcg(t.free_list + avail - 1 - k);
+        }
     }
-    // the slot of every row: the block from the table where the request held
-    // it already, else from the free list (the table entry may not be there yet)
-    const int rows = q.p.n_rows, rows_in = s_start[B];
-    for (int r = gtid; r < rows; r += gthreads) {
+    // the slot of every row, where they are few (else slots_kernel): the block
+    // from the table where the request held it already, else from the free list
+    // (the table entry may not be there yet)
+    const int rows_in = s_start[B];
+    for (int r = gtid; r < q.rows_here; r += gthreads) {
         int slot = -1;
         if (r < rows_in) {
             const int b = last_le(s_start, B + 1, r);
             const int n1 = s_n1[b], pos = n1 + (r - s_start[b]);
             if (pos < s_n2[b]) {
                 const int j = pos >> sh, held = blocks(n1);
-                const int id = j < held ? __ldcg(t.table + (size_t)b * W + j)
-                                        : __ldcg(t.free_list + avail - 1 - (s_need[b] + j - held));
-                slot = (int)((unsigned)id << sh) | (pos & (bs - 1));
-                if ((unsigned)id >= (unsigned)t.n_blocks) {
-                    atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
-                    slot = -1;
-                }
+                const int id = __ldcg(j < held ? t.table + (size_t)b * W + j
+                                               : t.free_list + avail - 1 - (s_need[b] + j - held));
+                if ((unsigned)id < (unsigned)t.n_blocks) slot = (id << sh) | (pos & (bs - 1));
+                else atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
             }
         }
         q.p.slot[r] = slot;
     }
     if (blockIdx.x != 0) return;
-    int took = 0;
+    long long took[1] = {0}, total_took[1];
     for (int b = b0; b < b1; ++b) {
         const int n0 = t.len[b];
         q.p.start[b] = s_start[b];
@@ -191,30 +215,93 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
         q.p.granted[b] = bad ? 0 : s_n2[b] - n0;
         if (!bad) {
             t.len[b] = s_n2[b];
-            took += blocks(s_n2[b]) - blocks(s_n1[b]);
+            took[0] += blocks(s_n2[b]) - blocks(s_n1[b]);
         }
     }
-    long long total_took;
-    block_exclusive_scan64(took, s_warp, &total_took);
+    block_exclusive_scan64<1>(took, s_warp + 96, total_took);
     if (tid == 0) {
         q.p.start[B] = s_start[B];
-        *t.n_free = avail - (int)total_took;
+        *t.n_free = avail - (int)total_took[0];
+    }
+}
+
+// The slot map of many rows, after the plan kernel: every request's blocks are in
+// the table by then.  A thread takes 8 consecutive rows: one search, the loads
+// independent of each other.  (On the plan kernel's 8 SMs this phase was 10 us of
+// a call's 13 for 151K rows.)
+constexpr int SLOT_THREADS = 256;
+
+__global__ void __launch_bounds__(SLOT_THREADS) slots_kernel(const __grid_constant__ PlanParams q) {
+    extern __shared__ int s_plan[];
+    const TableView& t = q.t;
+    const int B = t.B, tid = threadIdx.x, rows = q.p.n_rows;
+    int* s_start = s_plan;  // [B + 1]
+    pdl_wait();
+    for (int b = tid; b <= B; b += SLOT_THREADS) s_start[b] = q.p.start[b];
+    __syncthreads();
+    const int rows_in = s_start[B];
+    const bool vec = (reinterpret_cast<uintptr_t>(q.p.slot) & 15u) == 0;
+    for (long long r0 = ((long long)blockIdx.x * SLOT_THREADS + tid) * 8; r0 < rows;
+         r0 += (long long)gridDim.x * SLOT_THREADS * 8) {
+        int pos[8], id[8];
+        int b = r0 < rows_in ? last_le(s_start, B + 1, (int)r0) : B;
+        int n = 0, n0 = -1;  // the request's length now and before, once looked up
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = (int)r0 + k;
+            pos[k] = -1;
+            if (r0 + k < rows && r < rows_in) {
+                if (n0 < 0 || r >= s_start[b + 1]) {
+                    while (r >= s_start[b + 1]) ++b;
+                    n = t.len[b];
+                    n0 = n - max(q.p.granted[b], 0);
+                }
+                const int at = n0 + (r - s_start[b]);
+                if (at < n) {  // else refused
+                    pos[k] = at;
+                    id[k] = t.table[(size_t)b * t.max_blocks + (at >> t.sh)];
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            int slot = -1;
+            if (pos[k] >= 0) {
+                if ((unsigned)id[k] < (unsigned)t.n_blocks) slot = (id[k] << t.sh) | (pos[k] & (t.block - 1));
+                else atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
+            }
+            pos[k] = slot;
+        }
+        if (vec && r0 + 8 <= rows) {
+            int4* dst = reinterpret_cast<int4*>(q.p.slot + r0);
+            dst[0] = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            dst[1] = make_int4(pos[4], pos[5], pos[6], pos[7]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (r0 + k < rows) q.p.slot[r0 + k] = pos[k];
+        }
     }
 }
 
 cudaError_t launch_plan_blocks(const TableView& t, const int32_t* add, const PlanView& p, cudaStream_t st) {
     static LaunchCache lc;
-    const PlanParams q{t, p, add};
+    // few rows: one block and one launch.  Many: a cluster for the blocks, then the
+    // slot map on the whole GPU.
+    const bool many = p.n_rows > 4 * PLAN_THREADS;
+    const PlanParams q{t, p, add, many ? 0 : p.n_rows};
     const size_t smem = (5 * (size_t)t.B + 3) * 4;
     cudaError_t e = prepare_launch(plan_kernel, lc, smem, PLAN_THREADS, nullptr, nullptr);
     if (e != cudaSuccess) return e;
-    // one block until its threads write several slots each, then the cluster
-    const int ctas = p.n_rows > 4 * PLAN_THREADS ? PLAN_CLUSTER : 1;
+    // (a call that only drops may give back as many blocks as the table has)
+    const bool drops = p.n_rows == 0 && (long long)t.B * t.max_blocks > 8 * PLAN_THREADS;
+    const int ctas = many || drops || t.B > PLAN_THREADS ? PLAN_CLUSTER : 1;
+    const int threads = t.B <= 256 && p.n_rows <= 1024 && ctas == 1 ? 256 : PLAN_THREADS;  // barriers of fewer warps: 0.6 us less
     const bool timed = timing_enabled();
     if (timed && (e = timing_mark(KK_UPDATE, true, st)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(PLAN_THREADS);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -228,7 +315,14 @@ cudaError_t launch_plan_blocks(const TableView& t, const int32_t* add, const Pla
     cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, plan_kernel, q);
     if (timed && e == cudaSuccess) e = timing_mark(KK_UPDATE, false, st);
-    return e;
+    if (e != cudaSuccess || !many) return e;
+    static LaunchCache slots_lc;
+    int per_sm = 0, sms = 0;
+    const size_t slots_smem = ((size_t)t.B + 1) * 4;
+    e = prepare_launch(slots_kernel, slots_lc, slots_smem, SLOT_THREADS, &per_sm, &sms);
+    if (e != cudaSuccess) return e;
+    const int grid = min(sms * per_sm, (p.n_rows + SLOT_THREADS * 8 - 1) / (SLOT_THREADS * 8));
+    return launch_pdl(KK_UPDATE, slots_kernel, dim3(grid), dim3(SLOT_THREADS), slots_smem, st, q);
 }
 
 // ---------------------------------------------------------------------------
@@ -238,7 +332,10 @@ cudaError_t launch_plan_blocks(const TableView& t, const int32_t* add, const Pla
 // laid end to end (a scan over the requests in every block), so long and short
 // requests share the grid evenly.
 // ---------------------------------------------------------------------------
-constexpr int APP_THREADS = 256;
+// Small blocks: while some wait at the reduction's barrier, others load (32768 rows
+// of 8 heads: 37 us, 0.82 of the copy rate; 40 with 256 threads, 65 with 512, and
+// 60 with 256 that load their next item ahead, for want of registers).
+constexpr int APP_THREADS = 128;
 
 struct AppendParams {
     Q8View c;
@@ -299,47 +396,46 @@ __global__ void __launch_bounds__(APP_THREADS) append_kernel(const __grid_consta
 
     const int r0 = tid / TPR, part = tid % TPR;
     const long long items = (long long)total * Hkv * 2;
-    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-        const int is_v = (int)(it & 1);
+    struct Item {
+        int lo, hi;   // new rows of the block
+        int unit;     // block id * Hkv + head; -1: a bad slot
+        bool is_v;
+    };
+    auto load = [&](long long it, Item& x, uint4 (&w)[NP]) {
         const int h = (int)((it >> 1) % Hkv), blk_no = (int)((it >> 1) / Hkv);
-        int b = 0;
-        {
-            int hi = B;
-            while (hi - b > 1) {
-                const int mid = (b + hi) >> 1;
-                if (s_items[mid] <= blk_no) b = mid;
-                else hi = mid;
-            }
-        }
+        const int b = last_le(s_items, B, blk_no);
         const int n = t.len[b], a = q.p.granted[b], start = q.p.start[b];
         const int n_old = n - a;
         const int j = n_old / BS + (blk_no - s_items[b]);
-        const int lo = max(n_old - j * BS, 0), hi = min(n - j * BS, BS);  // new rows of the block: [lo, hi)
-        const int first = j * BS + lo - n_old;                            // the first one's index among the request's
-        const int slot = q.p.slot[start + first];
-        const int id = slot / BS;
-        if (slot < 0 || id >= t.n_blocks || slot % BS != lo) {  // uniform over the block
-            if (tid == 0) atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
-            continue;
-        }
-        const T* src = static_cast<const T*>(is_v ? q.r.v : q.r.k) + h * q.r.sh + part * V +
+        x.is_v = it & 1;
+        x.lo = max(n_old - j * BS, 0);
+        x.hi = min(n - j * BS, BS);
+        const int first = j * BS + x.lo - n_old;  // the first new row's index among the request's
+        const int slot = q.p.slot[start + first], id = slot / BS;
+        x.unit = slot < 0 || id >= t.n_blocks || slot % BS != x.lo ? -1 : id * Hkv + h;
+        const T* src = static_cast<const T*>(x.is_v ? q.r.v : q.r.k) + h * q.r.sh + part * V +
                        (q.r.T_rows ? b * q.r.sb + first * q.r.st : (int64_t)(start + first) * q.r.st);
-        uint4 w[NP];
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             const int r = p * RPP + r0;
             w[p] = make_uint4(0, 0, 0, 0);
-            if (r >= lo && r < hi) w[p] = *reinterpret_cast<const uint4*>(src + (int64_t)(r - lo) * q.r.st);
+            if (r >= x.lo && r < x.hi) w[p] = *reinterpret_cast<const uint4*>(src + (int64_t)(r - x.lo) * q.r.st);
         }
-        float* scale = (is_v ? q.c.v_scale : q.c.k_scale) + (size_t)id * Hkv + h;
-        const float s_old = lo > 0 ? *scale : 0.f;
+    };
+    auto store = [&](const Item& x, const uint4 (&w)[NP]) {
+        if (x.unit < 0) {  // uniform over the block
+            if (tid == 0) atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
+            return;
+        }
+        float* scale = (x.is_v ? q.c.v_scale : q.c.k_scale) + x.unit;
+        const float s_old = x.lo > 0 ? *scale : 0.f;
         unsigned amax = 0;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            float x[V];
-            vec16_values<T>(w[p], x);
+            float y[V];
+            vec16_values<T>(w[p], y);
 #pragma unroll
-            for (int i = 0; i < V; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
+            for (int i = 0; i < V; ++i) amax = max(amax, __float_as_uint(y[i]) & 0x7fffffffu);
         }
         amax = __reduce_max_sync(FULL, amax);
         if (lane == 0) s_max[warp] = amax;
@@ -347,38 +443,43 @@ __global__ void __launch_bounds__(APP_THREADS) append_kernel(const __grid_consta
         amax = __reduce_max_sync(FULL, s_max[lane % (APP_THREADS / 32)]);
         __syncthreads();  // s_max is free for the next item; every thread has the old scale
         float s = q8c_scale<FMT>(amax);
-        if (lo > 0 && !(s_old <= s)) s = s_old != s_old || s_old > s ? s_old : s;  // a NaN on either side stays
+        if (x.lo > 0 && !(s_old <= s)) s = s_old != s_old || s_old > s ? s_old : s;  // a NaN on either side stays
         const float inv = __fdiv_rn(1.f, s);
-        unsigned char* dst = static_cast<unsigned char*>(is_v ? q.c.v : q.c.k) +
-                             ((size_t)id * Hkv + h) * (BS * D) + part * V;
-        if (lo > 0 && s != s_old) {
+        unsigned char* dst = static_cast<unsigned char*>(x.is_v ? q.c.v : q.c.k) + (size_t)x.unit * (BS * D) + part * V;
+        if (x.lo > 0 && s != s_old) {
             // the block's older codes move to the larger scale
             const float f = __fmul_rn(s_old, inv);
-            for (int r = r0; r < lo; r += RPP) {
+            for (int r = r0; r < x.lo; r += RPP) {
                 unsigned* c = reinterpret_cast<unsigned*>(dst + r * D);
 #pragma unroll
                 for (int i = 0; i < V / 4; ++i) {
-                    float x[4];
-                    q8c_values<FMT>(c[i], x);
-                    c[i] = q8c_codes<FMT>(x[0], x[1], x[2], x[3], f);
+                    float y[4];
+                    q8c_values<FMT>(c[i], y);
+                    c[i] = q8c_codes<FMT>(y[0], y[1], y[2], y[3], f);
                 }
             }
         }
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             const int r = p * RPP + r0;
-            if (r >= lo && r < hi) {
-                float x[V];
-                vec16_values<T>(w[p], x);
+            if (r >= x.lo && r < x.hi) {
+                float y[V];
+                vec16_values<T>(w[p], y);
                 unsigned c[V / 4];
 #pragma unroll
                 for (int i = 0; i < V / 4; ++i)
-                    c[i] = q8c_codes<FMT>(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3], inv);
+                    c[i] = q8c_codes<FMT>(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3], inv);
                 if constexpr (V == 8) *reinterpret_cast<uint2*>(dst + r * D) = make_uint2(c[0], c[1]);
                 else *reinterpret_cast<unsigned*>(dst + r * D) = c[0];
             }
         }
         if (tid == 0) *scale = s;
+    };
+    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+        Item x;
+        uint4 w[NP];
+        load(it, x, w);
+        store(x, w);
     }
 }
 

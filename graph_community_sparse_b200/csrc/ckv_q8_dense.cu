@@ -23,11 +23,11 @@
 
 namespace ckv {
 
-constexpr int QD_WARPS = 6;
+constexpr int QD_WARPS = 4;
 constexpr int QD_THREADS = QD_WARPS * 32;
-constexpr int QD_CTAS = 2;          // resident blocks per SM
-constexpr int QD_MAX_GRID = 320;    // >= QD_CTAS * SMs
-constexpr int QD_MIN_PIECE = 24;    // tiles: below it more partials cost more than they save
+constexpr int QD_CTAS = 3;          // resident blocks per SM
+constexpr int QD_MAX_GRID = 480;    // >= QD_CTAS * SMs
+constexpr int QD_MIN_PIECE = 12;    // tiles: below it more partials cost more than they save
 constexpr int QD_CROSS = 12;        // tiles: what crossing a unit costs a block
 
 template <int D>
