@@ -39,26 +39,25 @@ __device__ __forceinline__ void sparse_q8_segment(const SparseQ8Params& p, int u
     const auto raw_q = Q8Warp<D, GQ, FMT>::fetch_q(
         Q8Warp<D, GQ, FMT>::q_row(p.d.q, p.c.dtype, (size_t)b * p.d.Hq + h0), p.c.dtype, lane);
 
-    // a tile's 32 list entries, one a lane: positions two tiles ahead of the
-    // copies, pool rows (-1: not attended) one tile ahead
-    auto positions = [&](int i) { return i * Q8_TOK + lane < n ? toks[lo + i * Q8_TOK + lane] : -1; };
-    auto rows = [&](int pos, int i) {
-        int row = -1;
-        if ((unsigned)pos < (unsigned)max(len, 0)) {
-            const int id = table[pos >> t.sh];
-            if ((unsigned)id < (unsigned)t.n_blocks) row = ((id * p.c.Hkv + kvh) << t.sh) + (pos & (t.block - 1));
-        }
-        if (row < 0 && i * Q8_TOK + lane < n) atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
-        return row;
-    };
-    int pos_nxt = positions(1);
-    int row_nxt = rows(positions(0), 0);
+    // a tile's 32 list entries, one a lane.  Tile i's copies need its positions
+    // and their blocks: loaded two and one tiles ahead, and only looked at by the
+    // copies themselves, so that no load is waited for where it is issued.
+    auto position = [&](int i) { return i * Q8_TOK + lane < n ? toks[lo + i * Q8_TOK + lane] : -1; };
+    auto inside = [&](int pos) { return (unsigned)pos < (unsigned)max(len, 0); };
+    auto block_of = [&](int pos) { return inside(pos) ? table[pos >> t.sh] : -1; };
+    int pos0 = position(0), pos1 = position(1);
+    int id0 = block_of(pos0);
     int stage_in = 0;
     auto issue = [&](int i) {
         if (i < nit) {
-            const int row_cur = row_nxt;
-            row_nxt = rows(pos_nxt, i + 1);
-            pos_nxt = positions(i + 2);
+            int row_cur = -1;  // the entry's row of the pool; -1: not attended
+            if (inside(pos0) && (unsigned)id0 < (unsigned)t.n_blocks)
+                row_cur = ((id0 * p.c.Hkv + kvh) << t.sh) + (pos0 & (t.block - 1));
+            else if (i * Q8_TOK + lane < n)
+                atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
+            pos0 = pos1;
+            id0 = block_of(pos0);
+            pos1 = position(i + 2);
             unsigned char* slot_p = ring + stage_in * QG::SLOT;
             const unsigned sm = smem_addr32(slot_p);
 #pragma unroll
