@@ -45,17 +45,17 @@
 namespace ckv {
 
 constexpr int Q8_HALF = 16;  // tokens of a product's tile
-constexpr int Q8_TOK = 32;   // tokens of a staged tile: two of those
 constexpr float Q8_M_INIT = -1e30f;
 
-template <int D>
+// A staged tile of NH such halves (1 or 2).
+template <int D, int NH>
 struct Q8Geom {
+    static constexpr int TOK = NH * Q8_HALF;
     static constexpr int HALF = Q8_HALF * D;       // bytes of 16 rows
-    static constexpr int V = 2 * HALF;             // K's two halves, then V's
+    static constexpr int V = NH * HALF;            // K's halves, then V's
     static constexpr int CH = D / 16;              // 16-byte chunks per row
-    static constexpr int SCALES = 4 * HALF;        // float [32] of K, then of V
-    static constexpr int MASK = SCALES + 256;      // 32 bits (sparse): the tokens that count
-    static constexpr int SLOT = SCALES + 384;      // bytes of a ring slot (a multiple of 128)
+    static constexpr int SCALES = 2 * NH * HALF;   // float [NH][2]: K's and V's scale of each half (dense)
+    static constexpr int SLOT = SCALES + 128;      // bytes of a ring slot (a multiple of 128)
     static constexpr int KS = D / 16;              // k-steps of Q K^T
     static constexpr int MT = D / 16;              // 16-dim tiles of V^T
 };
@@ -203,9 +203,9 @@ __device__ __forceinline__ void cp_async_4p(unsigned s, const void* g, bool pred
 }
 
 // The state of one warp over one unit's tokens: lane 4 g + t.
-template <int D, int GQ, int FMT>
+template <int D, int GQ, int FMT, int NH>
 struct Q8Warp {
-    using QG = Q8Geom<D>;
+    using QG = Q8Geom<D, NH>;
     static constexpr bool SPLIT = GQ == 8;  // hi and lo in products of their own
     unsigned qh[QG::KS][2];                 // Q^T fragments (SPLIT: hi; else hi in columns 0..3, lo or hi again in 4..7)
     unsigned ql[SPLIT ? QG::KS : 1][2];
@@ -328,12 +328,15 @@ struct Q8Warp {
     }
 
     // One tile staged at sm; mask: which of its tokens count.  UNIFORM: the 16
-    // tokens of a half have one scale each for K and V.  lam (NEIGHBOURS): lam(i, x)
-    // receives the largest x over the group's heads of the tile's token i, from
-    // one lane per token.  Two halves at a time give the products independent work
-    // and share the checks, the loads' bookkeeping and the fp32 additions.
+    // tokens of a half have one scale each for K and V, staged with the tile;
+    // otherwise (NH = 1) lane i has the K scale of token i, lane 16 + i its V scale
+    // in `scale`.  lam (NEIGHBOURS): lam(i, x) receives the largest x over the group's
+    // heads of the tile's token i, from one lane per token.  Two halves at a time
+    // give the products independent work and share the checks, the loads'
+    // bookkeeping and the fp32 additions.
     template <bool UNIFORM, bool NEIGHBOURS, typename Lam>
-    __device__ __forceinline__ void tile(unsigned sm, unsigned mask, int lane, Lam lam) {
+    __device__ __forceinline__ void tile(unsigned sm, unsigned mask, float scale, int lane, Lam lam) {
+        static_assert(UNIFORM || NH == 1, "a lane per scale");
         const int g = lane >> 2, t = lane & 3;
         if (mask == 0u) return;  // uniform over the warp
         // rows 8 apart are 8 D bytes apart; chunks t and t + 4 (d = 128) differ in bit 6,
@@ -341,9 +344,9 @@ struct Q8Warp {
         const unsigned ks = sm + q8_swz<D>(g, t), ks2 = sm + (q8_swz<D>(g, t) ^ 64);
 
         // S: rows g, g + 8 of each half, columns 2t, 2t + 1; even and odd k-steps apart
-        float s[2][2][2];  // [half][token g | g + 8][head]
+        float s[NH][2][2];  // [half][token g | g + 8][head]
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < NH; ++j) {
             float sa[4] = {s0[0], s0[1], s0[0], s0[1]}, sb[4];
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
@@ -368,25 +371,30 @@ struct Q8Warp {
         }
         if (!SPLIT && q_lo) {  // uniform
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 4 * NH; ++i)
                 s[i >> 2][i >> 1 & 1][i & 1] += __shfl_xor_sync(FULL, s[i >> 2][i >> 1 & 1][i & 1], 2);
         }
         constexpr int NS = UNIFORM ? 1 : 2;
-        float vs[2][NS], kf[2][NS][2];
+        float vs[NH][NS], kf[NH][NS][2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NH; ++j)
 #pragma unroll
             for (int r = 0; r < NS; ++r) {
-                const unsigned at = sm + QG::SCALES + 64 * j + (UNIFORM ? 0 : 4 * (g + 8 * r));
-                const float kscale = lds32f(at);
-                vs[j][r] = lds32f(at + 128);
+                float kscale;
+                if constexpr (UNIFORM) {
+                    kscale = lds32f(sm + QG::SCALES + 8 * j);
+                    vs[j][r] = lds32f(sm + QG::SCALES + 8 * j + 4);
+                } else {
+                    kscale = __shfl_sync(FULL, scale, g + 8 * r);
+                    vs[j][r] = __shfl_sync(FULL, scale, 16 + g + 8 * r);
+                }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) kf[j][r][e] = kscale * qf[e];
             }
         auto on = [&](int j, int r) { return (mask >> (16 * j + 8 * r + g) & 1u) != 0u; };
-        if (mask != 0xffffffffu) {  // uniform
+        if (mask != (NH == 2 ? 0xffffffffu : 0xffffu)) {  // uniform
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < NH; ++j)
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -399,7 +407,7 @@ struct Q8Warp {
 
         if constexpr (NEIGHBOURS) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < NH; ++j)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     float v = -INFINITY;
@@ -412,12 +420,12 @@ struct Q8Warp {
                 }
         }
 
-        float p[2][2][2], w[2][2][2];
+        float p[NH][2][2], w[NH][2][2];
         auto weights = [&]() {
-            float cv[2][NS][2];
+            float cv[NH][NS][2];
             bool high = false, wide = false;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < NH; ++j)
 #pragma unroll
                 for (int r = 0; r < NS; ++r)
 #pragma unroll
@@ -426,7 +434,7 @@ struct Q8Warp {
                         wide = wide || cv[j][r][e] > 128.f;
                     }
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < NH; ++j)
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -438,7 +446,7 @@ struct Q8Warp {
                     }
             if (__any_sync(FULL, wide)) {  // with p <= 2^8 only these can pass 2^15
 #pragma unroll
-                for (int i = 0; i < 8; ++i) high = high || w[i >> 2][i >> 1 & 1][i & 1] > 32768.f;
+                for (int i = 0; i < 4 * NH; ++i) high = high || w[i >> 2][i >> 1 & 1][i & 1] > 32768.f;
             }
             return __any_sync(FULL, high);
         };
@@ -449,7 +457,7 @@ struct Q8Warp {
             for (int e = 0; e < 2; ++e) {
                 float mx = Q8_M_INIT, mv = Q8_M_INIT;
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < NH; ++j)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const float x = s[j][r][e] * kf[j][r % NS][e];
@@ -482,12 +490,16 @@ struct Q8Warp {
             weights();
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) l[e] += (p[0][0][e] + p[0][1][e]) + (p[1][0][e] + p[1][1][e]);
+        for (int e = 0; e < 2; ++e) {
+            float x = p[0][0][e] + p[0][1][e];
+            if constexpr (NH == 2) x += p[1][0][e] + p[1][1][e];
+            l[e] += x;
+        }
 
         // P fragments: token pairs of column g
-        unsigned b[2][SPLIT ? 2 : 1][2];
+        unsigned b[NH][SPLIT ? 2 : 1][2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NH; ++j)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const unsigned hi = pack_half2(w[j][r][0], w[j][r][1]);
@@ -501,34 +513,39 @@ struct Q8Warp {
                 }
             }
         // O: lane's codes are dims (d/8) g + 0..d/8-1 of tokens 2t, 2t+1, 2t+8, 2t+9 of each half
-        unsigned vw[2][4][D / 32];
+        unsigned vw[NH][4][D / 32];
         {
-            constexpr int N = 8 * D, H = QG::HALF;  // 8 rows on; the other half
-            if constexpr (D == 128) {
-                const unsigned v0 = sm + QG::V + q8_swz<D>(2 * t, g), v1 = sm + QG::V + (q8_swz<D>(2 * t, g) ^ 64);
-                const uint4 x[8] = {lds128<0>(v0),     lds128<128>(v1),     lds128<N>(v0),     lds128<N + 128>(v1),
-                                    lds128<H>(v0),     lds128<H + 128>(v1), lds128<H + N>(v0), lds128<H + N + 128>(v1)};
+            constexpr int N = 8 * D;  // 8 rows on
+            const int at = D == 128 ? q8_swz<D>(2 * t, g) : q8_swz<D>(2 * t, g >> 1);
+            const unsigned low = sm + QG::V + (D == 128 ? 0 : 8 * (g & 1));
+            const unsigned v0 = low + at, v1 = low + (at ^ 64);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    vw[k >> 2][k & 3][0] = x[k].x; vw[k >> 2][k & 3][1] = x[k].y;
-                    vw[k >> 2][k & 3][2] = x[k].z; vw[k >> 2][k & 3][3] = x[k].w;
-                }
-            } else {
-                const unsigned v0 = sm + QG::V + q8_swz<D>(2 * t, g >> 1) + 8 * (g & 1);
-                const unsigned v1 = sm + QG::V + (q8_swz<D>(2 * t, g >> 1) ^ 64) + 8 * (g & 1);
-                const uint2 x[8] = {lds64<0>(v0), lds64<0>(v1), lds64<N>(v0),     lds64<N>(v1),
-                                    lds64<H>(v0), lds64<H>(v1), lds64<H + N>(v0), lds64<H + N>(v1)};
+            for (int j = 0; j < NH; ++j) {
+                if constexpr (D == 128) {
+                    const uint4 x[4] = {j ? lds128<QG::HALF>(v0) : lds128<0>(v0),
+                                        j ? lds128<QG::HALF + 128>(v1) : lds128<128>(v1),
+                                        j ? lds128<QG::HALF + N>(v0) : lds128<N>(v0),
+                                        j ? lds128<QG::HALF + N + 128>(v1) : lds128<N + 128>(v1)};
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    vw[k >> 2][k & 3][0] = x[k].x; vw[k >> 2][k & 3][1] = x[k].y;
+                    for (int k = 0; k < 4; ++k) {
+                        vw[j][k][0] = x[k].x; vw[j][k][1] = x[k].y; vw[j][k][2] = x[k].z; vw[j][k][3] = x[k].w;
+                    }
+                } else {
+                    const uint2 x[4] = {j ? lds64<QG::HALF>(v0) : lds64<0>(v0), j ? lds64<QG::HALF>(v1) : lds64<0>(v1),
+                                        j ? lds64<QG::HALF + N>(v0) : lds64<N>(v0),
+                                        j ? lds64<QG::HALF + N>(v1) : lds64<N>(v1)};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        vw[j][k][0] = x[k].x; vw[j][k][1] = x[k].y;
+                    }
                 }
             }
         }
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-            unsigned a[2][2][4];  // [half][tokens 2t, 2t + 1 | 2t + 8, 2t + 9][code of the word]
+            unsigned a[NH][2][4];  // [half][tokens 2t, 2t + 1 | 2t + 8, 2t + 9][code of the word]
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < NH; ++j) {
                 q8_v_halves<FMT>(vw[j][0][i], vw[j][1][i], a[j][0]);
                 q8_v_halves<FMT>(vw[j][2][i], vw[j][3][i], a[j][1]);
             }
@@ -539,7 +556,7 @@ struct Q8Warp {
                 // tiles of a long request would cost 4e-6 of the output
                 float d[4];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < NH; ++j)
 #pragma unroll
                     for (int y = 0; y < (SPLIT ? 2 : 1); ++y) {
                         if (j == 0 && y == 0)

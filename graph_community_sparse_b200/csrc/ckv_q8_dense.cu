@@ -23,6 +23,7 @@
 
 namespace ckv {
 
+constexpr int QD_TOK = 32;          // tokens of a tile
 constexpr int QD_WARPS = 4;
 constexpr int QD_THREADS = QD_WARPS * 32;
 constexpr int QD_CTAS = 3;          // resident blocks per SM
@@ -53,7 +54,7 @@ size_t q8_dense_ws_bytes(int gq, int d) {
 
 template <int D, int GQ>
 struct DenseQ8Smem {
-    static constexpr int WARP = QdStages<D>::v * Q8Geom<D>::SLOT;  // a warp's ring, then its accumulators
+    static constexpr int WARP = QdStages<D>::v * Q8Geom<D, 2>::SLOT;  // a warp's ring, then its accumulators
     static constexpr int FIXED = QD_WARPS * WARP + 2 * QD_WARPS * GQ * 4;
     static_assert(GQ * D * 4 <= WARP, "a warp's accumulators fit its ring");
     // the join of a unit's partials: weights and sums of JOIN slots at a time
@@ -170,8 +171,8 @@ __device__ __forceinline__ void join_partials(const DenseQ8Params& p, int c0, in
 // them), to sm + SO.  Rows 4 apart (d = 128) differ in the swizzle by one bit.
 template <int D, int SO>
 __device__ __forceinline__ void copy_half(unsigned sm, const char* k, const char* v, int lane) {
-    constexpr int V = Q8Geom<D>::V + SO;
-    const unsigned even = sm + q8_swz<D>(lane / Q8Geom<D>::CH, lane % Q8Geom<D>::CH);
+    constexpr int V = Q8Geom<D, 2>::V + SO;
+    const unsigned even = sm + q8_swz<D>(lane / Q8Geom<D, 2>::CH, lane % Q8Geom<D, 2>::CH);
     cp_async_16i<SO, 0>(even, k);
     cp_async_16i<V, 0>(even, v);
     if constexpr (D == 128) {
@@ -190,7 +191,7 @@ __device__ __forceinline__ void copy_half(unsigned sm, const char* k, const char
 
 template <int D, int GQ, int FMT>
 __global__ void __launch_bounds__(QD_THREADS, QD_CTAS) dense_q8_kernel(const __grid_constant__ DenseQ8Params p) {
-    using QG = Q8Geom<D>;
+    using QG = Q8Geom<D, 2>;
     using SM = DenseQ8Smem<D, GQ>;
     constexpr int STAGES = QdStages<D>::v;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(QD_THREADS, QD_CTAS) dense_q8_kernel(const __g
         const int n = t.len[b];
         const bool ok = n >= 0 && n <= (long long)t.max_blocks * bs;
         if (!ok && blockIdx.x == 0) atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
-        s_nt[b] = ok ? (n + Q8_TOK - 1) / Q8_TOK : 0;
+        s_nt[b] = ok ? (n + QD_TOK - 1) / QD_TOK : 0;
     }
     __syncthreads();
     // from here every warp works for itself, 32 requests at a time
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(QD_THREADS, QD_CTAS) dense_q8_kernel(const __g
         if (s_nt[b] == 0)  // nothing to attend to
             for (int i = tid; i < p.c.Hq * D; i += QD_THREADS) p.out[(size_t)b * p.c.Hq * D + i] = 0.f;
 
-    Q8Warp<D, GQ, FMT> st;
+    Q8Warp<D, GQ, FMT, 2> st;
     for (int at = start; at < end;) {
         // the segment: tiles [lo, hi) of KV head h of request b, the unit shared by the blocks c0 .. c0 + np - 1
         int b = 0, pre = 0;  // pre: what comes before request b
@@ -286,15 +287,15 @@ __global__ void __launch_bounds__(QD_THREADS, QD_CTAS) dense_q8_kernel(const __g
             slot += at == start ? 0 : 1;
             at = ubeg + hi;
         }
-        const auto raw_q = Q8Warp<D, GQ, FMT>::fetch_q(
-            Q8Warp<D, GQ, FMT>::q_row(p.q, p.c.dtype, (size_t)b * p.c.Hq + h * GQ), p.c.dtype, lane);
+        const auto raw_q = Q8Warp<D, GQ, FMT, 2>::fetch_q(
+            Q8Warp<D, GQ, FMT, 2>::q_row(p.q, p.c.dtype, (size_t)b * p.c.Hq + h * GQ), p.c.dtype, lane);
         const int n = t.len[b];
         const int32_t* table = t.table + (size_t)b * t.max_blocks;
 
         const int nit = (hi - lo - warp + QD_WARPS - 1) / QD_WARPS;  // this warp's tiles: lo + warp + QD_WARPS i
         // a window of 16 tiles: lane 2 i + j holds the block of half j of this warp's tile i
         auto block_of = [&](int x) {
-            const int pos = (lo + warp + QD_WARPS * (x + (lane >> 1))) * Q8_TOK + (lane & 1) * Q8_HALF;
+            const int pos = (lo + warp + QD_WARPS * (x + (lane >> 1))) * QD_TOK + (lane & 1) * Q8_HALF;
             return x + (lane >> 1) < nit && pos < n ? table[pos >> t.sh] : 0;
         };
         int win_cur = block_of(0), win_nxt = block_of(16);
@@ -312,16 +313,16 @@ __global__ void __launch_bounds__(QD_THREADS, QD_CTAS) dense_q8_kernel(const __g
                 }
                 const unsigned sm = ring32 + stage_in * QG::SLOT;
                 const int id0 = __shfl_sync(FULL, win_cur, 2 * (x & 15)), id1 = __shfl_sync(FULL, win_cur, 2 * (x & 15) + 1);
-                const int pos = (lo + warp + QD_WARPS * x) * Q8_TOK;
+                const int pos = (lo + warp + QD_WARPS * x) * QD_TOK;
                 const bool ok0 = (unsigned)id0 < (unsigned)t.n_blocks, ok1 = (unsigned)id1 < (unsigned)t.n_blocks;
                 const unsigned unit0 = id0 * Hkv + h, unit1 = id1 * Hkv + h;
                 const size_t src0 = (size_t)((unit0 << t.sh) + (pos & (bs - 1))) * D;
                 const size_t src1 = (size_t)((unit1 << t.sh) + ((pos + Q8_HALF) & (bs - 1))) * D;
-                if (pos + Q8_TOK <= n && ok0 && ok1) {
+                if (pos + QD_TOK <= n && ok0 && ok1) {
                     copy_half<D, 0>(sm, klane + src0, vlane + src0, lane);
                     copy_half<D, QG::HALF>(sm, klane + src1, vlane + src1, lane);
                     bad &= ~(3u << 2 * stage_in);
-                    cp_async_4p(sm + QG::SCALES + lane * 64, slane + (lane & 1 ? unit1 : unit0), lane < 4);
+                    cp_async_4p(sm + QG::SCALES + 8 * (lane & 1) + 4 * (lane >> 1), slane + (lane & 1 ? unit1 : unit0), lane < 4);
                 } else {
                     // the end of the request, or a block out of range: zeros where there is nothing
 #pragma unroll
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(QD_THREADS, QD_CTAS) dense_q8_kernel(const __g
                             cp_async_16s(dst + QG::V, vlane + from, size);
                         }
                         if (lane < 2)
-                            cp_async_4s(sm + QG::SCALES + 64 * j + 128 * lane,
+                            cp_async_4s(sm + QG::SCALES + 8 * j + 4 * lane,
                                         (lane ? p.c.v_scale : p.c.k_scale) + (rows > 0 ? (j ? unit1 : unit0) : 0),
                                         rows > 0 ? 4 : 0);
                     }
@@ -355,17 +356,17 @@ __global__ void __launch_bounds__(QD_THREADS, QD_CTAS) dense_q8_kernel(const __g
         st.set_q(raw_q, p.c.dtype, p.scale_log2, lane);
         st.reset();
         unsigned stage_out = 0;
-        int left = n - (lo + warp) * Q8_TOK;  // tokens from this tile's first on
+        int left = n - (lo + warp) * QD_TOK;  // tokens from this tile's first on
         for (int x = 0; x < nit; ++x) {
             __syncwarp();  // every lane is done reading the slot refilled next
             issue(x + STAGES - 1);
             cp_async_wait<STAGES - 1>();
             __syncwarp();  // what the other lanes copied is visible
             unsigned mask = 0xffffffffu;
-            if (left < Q8_TOK) mask >>= Q8_TOK - left;
+            if (left < QD_TOK) mask >>= QD_TOK - left;
             if (bad) mask &= ~((bad >> 2 * stage_out & 1u) * 0xffffu | (bad >> 2 * stage_out & 2u) * 0x7fff8000u);
-            st.template tile<true, false>(ring32 + stage_out * QG::SLOT, mask, lane, [](int, float) {});
-            left -= QD_WARPS * Q8_TOK;
+            st.template tile<true, false>(ring32 + stage_out * QG::SLOT, mask, 0.f, lane, [](int, float) {});
+            left -= QD_WARPS * QD_TOK;
             stage_out = stage_out + 1 == STAGES ? 0 : stage_out + 1;
         }
         cp_async_wait<0>();
@@ -423,7 +424,7 @@ static cudaError_t launch_dense_q8_t(const DenseQ8Params& p, cudaStream_t st) {
     cudaError_t e = prepare_launch(kern, lc, smem, QD_THREADS, &per_sm, &sms);
     if (e != cudaSuccess) return e;
     if (sms <= 0 || per_sm <= 0) return cudaErrorInvalidConfiguration;
-    const long long tiles = (long long)p.c.t.B * p.c.Hkv * p.c.t.max_blocks * p.c.t.block / Q8_TOK + (long long)p.c.t.B * p.c.Hkv;
+    const long long tiles = (long long)p.c.t.B * p.c.Hkv * p.c.t.max_blocks * p.c.t.block / QD_TOK + (long long)p.c.t.B * p.c.Hkv;
     const int grid = (int)min((long long)min(sms * per_sm, QD_MAX_GRID), (tiles + QD_MIN_PIECE - 1) / QD_MIN_PIECE);
     return launch_pdl(KK_ATTENTION, kern, dim3(grid), dim3(QD_THREADS), smem, st, p);
 }

@@ -16,8 +16,9 @@
 namespace ckv {
 
 constexpr int QS_WARPS = 4;
-constexpr int QS_STAGES = 2;
-constexpr int QS_CTAS = 3;  // resident blocks per SM
+constexpr int QS_TOK = 16;    // tokens of a tile: 16 warps an SM then have room for three
+constexpr int QS_STAGES = 3;
+constexpr int QS_CTAS = 4;    // resident blocks per SM
 
 struct SparseQ8Params {
     DecodeParams d;
@@ -27,80 +28,92 @@ struct SparseQ8Params {
 template <int D, int GQ, int FMT>
 __device__ __forceinline__ void sparse_q8_segment(const SparseQ8Params& p, int u, int lo, int hi, int slot,
                                                   unsigned char* ring, int lane) {
-    using QG = Q8Geom<D>;
+    using QG = Q8Geom<D, 1>;
     const TableView& t = p.c.t;
     int b, kvh, h0;
     unit_heads(p.d, u, GQ, false, b, kvh, h0);
     const int32_t* toks = p.d.sel_tok + (size_t)u * p.d.tok_cap;
     const int32_t* table = t.table + (size_t)b * t.max_blocks;
     const int len = (int)min((long long)t.len[b], (long long)t.max_blocks << t.sh);
-    const int n = hi - lo, nit = (n + Q8_TOK - 1) / Q8_TOK;
+    const int n = hi - lo, nit = (n + QS_TOK - 1) / QS_TOK;
 
-    const auto raw_q = Q8Warp<D, GQ, FMT>::fetch_q(
-        Q8Warp<D, GQ, FMT>::q_row(p.d.q, p.c.dtype, (size_t)b * p.d.Hq + h0), p.c.dtype, lane);
+    const auto raw_q = Q8Warp<D, GQ, FMT, 1>::fetch_q(
+        Q8Warp<D, GQ, FMT, 1>::q_row(p.d.q, p.c.dtype, (size_t)b * p.d.Hq + h0), p.c.dtype, lane);
 
-    // a tile's 32 list entries, one a lane.  Tile i's copies need its positions
-    // and their blocks: loaded two and one tiles ahead, and only looked at by the
-    // copies themselves, so that no load is waited for where it is issued.
-    auto position = [&](int i) { return i * Q8_TOK + lane < n ? toks[lo + i * Q8_TOK + lane] : -1; };
+    // Two tiles' entries are a window, one entry a lane.  The copies of a window
+    // need its positions and their blocks: loaded two and one windows ahead, and
+    // only looked at by the copies themselves, so that no load is waited for where
+    // it is issued.
+    auto position = [&](int w) { return w * 32 + lane < n ? toks[lo + w * 32 + lane] : -1; };
     auto inside = [&](int pos) { return (unsigned)pos < (unsigned)max(len, 0); };
     auto block_of = [&](int pos) { return inside(pos) ? table[pos >> t.sh] : -1; };
     int pos0 = position(0), pos1 = position(1);
     int id0 = block_of(pos0);
-    int stage_in = 0;
+    int row_cur = -1;  // this window's entry's row of the pool; -1: not attended
+    // the tiles' scales (lanes 0..15 K's, 16..31 V's) and masks, newest first
+    float scales[QS_STAGES];
+    unsigned masks[QS_STAGES];
+    const float* slane = lane < 16 ? p.c.k_scale : p.c.v_scale;
+    const unsigned ring32 = smem_addr32(ring);
+    unsigned stage_in = 0;
     auto issue = [&](int i) {
-        if (i < nit) {
-            int row_cur = -1;  // the entry's row of the pool; -1: not attended
-            if (inside(pos0) && (unsigned)id0 < (unsigned)t.n_blocks)
-                row_cur = ((id0 * p.c.Hkv + kvh) << t.sh) + (pos0 & (t.block - 1));
-            else if (i * Q8_TOK + lane < n)
-                atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
-            pos0 = pos1;
-            id0 = block_of(pos0);
-            pos1 = position(i + 2);
-            unsigned char* slot_p = ring + stage_in * QG::SLOT;
-            const unsigned sm = smem_addr32(slot_p);
 #pragma unroll
-            for (int x = 0; x < 2 * QG::HALF / 512; ++x) {
+        for (int k = QS_STAGES - 1; k > 0; --k) {
+            scales[k] = scales[k - 1];
+            masks[k] = masks[k - 1];
+        }
+        if (i < nit) {
+            if ((i & 1) == 0) {
+                row_cur = -1;
+                if (inside(pos0) && (unsigned)id0 < (unsigned)t.n_blocks)
+                    row_cur = ((id0 * p.c.Hkv + kvh) << t.sh) + (pos0 & (t.block - 1));
+                else if (i * QS_TOK + lane < n)
+                    atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
+                pos0 = pos1;
+                id0 = block_of(pos0);
+                pos1 = position((i >> 1) + 2);
+            }
+            const unsigned sm = ring32 + stage_in * QG::SLOT;
+            const int base = (i & 1) << 4;
+            const int mine = __shfl_sync(FULL, row_cur, base + (lane & 15));
+            scales[0] = mine >= 0 ? slane[mine >> t.sh] : 0.f;
+            masks[0] = __ballot_sync(FULL, mine >= 0) & 0xffffu;
+#pragma unroll
+            for (int x = 0; x < QG::HALF / 512; ++x) {
                 const int idx = x * 32 + lane, r = idx / QG::CH, c = idx % QG::CH;
-                const int row = __shfl_sync(FULL, row_cur, r);
+                const int row = __shfl_sync(FULL, row_cur, base + r);
                 const int size = row >= 0 ? 16 : 0;
                 const size_t src = (size_t)max(row, 0) * D + c * 16;
-                const unsigned dst = sm + (r >> 4) * QG::HALF + q8_swz<D>(r & 15, c);
+                const unsigned dst = sm + q8_swz<D>(r, c);
                 cp_async_16s(dst, static_cast<const char*>(p.c.k) + src, size);
                 cp_async_16s(dst + QG::V, static_cast<const char*>(p.c.v) + src, size);
             }
-            const int unit = max(row_cur, 0) >> t.sh, size = row_cur >= 0 ? 4 : 0;
-            cp_async_4s(sm + QG::SCALES + lane * 4, p.c.k_scale + unit, size);
-            cp_async_4s(sm + QG::SCALES + 128 + lane * 4, p.c.v_scale + unit, size);
-            const unsigned mask = __ballot_sync(FULL, row_cur >= 0);
-            if (lane == 0) *reinterpret_cast<unsigned*>(slot_p + QG::MASK) = mask;
         }
         stage_in = stage_in + 1 == QS_STAGES ? 0 : stage_in + 1;
         cp_async_commit();
     };
 #pragma unroll
     for (int s = 0; s < QS_STAGES - 1; ++s) issue(s);
-    Q8Warp<D, GQ, FMT> st;
+    Q8Warp<D, GQ, FMT, 1> st;
     st.set_q(raw_q, p.c.dtype, p.d.scale_log2, lane);
     st.reset();
     float* lamu = p.d.ws.lam + (size_t)u * p.d.ws.lam_cap + lo;
-    int stage_out = 0;
+    unsigned stage_out = 0;
     auto step = [&](auto nbr) {
         for (int i = 0; i < nit; ++i) {
             __syncwarp();  // every lane is done reading the slot refilled next
             issue(i + QS_STAGES - 1);
             cp_async_wait<QS_STAGES - 1>();
             __syncwarp();  // what the other lanes copied is visible
-            const unsigned char* sm = ring + stage_out * QG::SLOT;
-            const unsigned mask = *reinterpret_cast<const unsigned*>(sm + QG::MASK);
+            const unsigned mask = masks[QS_STAGES - 1];
             if constexpr (decltype(nbr)::value) {
                 // an all-invalid tile has no logits of its own to store
-                if (mask == 0u && i * Q8_TOK + lane < n) lamu[i * Q8_TOK + lane] = -INFINITY;
+                if (mask == 0u && lane < QS_TOK && i * QS_TOK + lane < n) lamu[i * QS_TOK + lane] = -INFINITY;
             }
-            st.template tile<false, decltype(nbr)::value>(smem_addr32(sm), mask, lane, [&](int k, float x) {
-                if (i * Q8_TOK + k < n) lamu[i * Q8_TOK + k] = x;
-            });
+            st.template tile<false, decltype(nbr)::value>(
+                ring32 + stage_out * QG::SLOT, mask, scales[QS_STAGES - 1], lane, [&](int k, float x) {
+                    if (i * QS_TOK + k < n) lamu[i * QS_TOK + k] = x;
+                });
             stage_out = stage_out + 1 == QS_STAGES ? 0 : stage_out + 1;
         }
     };
@@ -115,7 +128,7 @@ template <int D, int GQ, int FMT>
 __global__ void __launch_bounds__(QS_WARPS * 32, QS_CTAS) sparse_q8_kernel(const __grid_constant__ SparseQ8Params p) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int s_warp[33];
-    constexpr int RING = QS_STAGES * Q8Geom<D>::SLOT;
+    constexpr int RING = QS_STAGES * Q8Geom<D, 1>::SLOT;
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     unsigned char* ring = smem + warp * RING;
@@ -180,7 +193,7 @@ template <int D, int GQ, int FMT>
 static cudaError_t launch_sparse_q8_t(SparseQ8Params p, cudaStream_t st) {
     static LaunchCache lc;
     auto kern = sparse_q8_kernel<D, GQ, FMT>;
-    const size_t smem = QS_WARPS * QS_STAGES * Q8Geom<D>::SLOT + ((size_t)p.d.U + 1) * 4;
+    const size_t smem = QS_WARPS * QS_STAGES * Q8Geom<D, 1>::SLOT + ((size_t)p.d.U + 1) * 4;
     int per_sm = 0, sms = 0;
     cudaError_t e = prepare_launch(kern, lc, smem, QS_WARPS * 32, &per_sm, &sms);
     if (e != cudaSuccess) return e;
