@@ -271,13 +271,13 @@ ckv_status check_q8_graph(const ckv_q8_desc* c, const ckv_graph_desc* g) {
 
 // head, counters, then the larger of the two calls' parts
 size_t q8_ws_bytes(const ckv_q8_desc* c, const ckv_graph_desc* g, int tok_cap) {
-    size_t need = ckv::q8_dense_ws_bytes(c->Hq / c->Hkv, c->d);
+    size_t need = ckv::q8_blocks_ws_bytes(c->Hq / c->Hkv, c->d);
     if (g) {
         const int G = g->mode == CKV_GRAPH_PER_HEAD ? c->Hq : c->Hkv;
         const size_t s = ckv::decode_ws_bytes(c->blocks.B * G, c->Hq / G, c->d, tok_cap);
         need = need > s ? need : s;
     }
-    return ckv::WS_RESERVED + ckv::q8_counter_bytes(c->blocks.B * c->Hkv) + need;
+    return ckv::WS_RESERVED + ckv::q8_counter_bytes(c->blocks.B * c->Hq) + need;
 }
 
 #define CKV_TRY(expr)                      \

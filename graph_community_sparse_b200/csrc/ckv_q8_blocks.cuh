@@ -1,0 +1,554 @@
+// The block-split attention over an 8-bit cache, sm_100a: all tokens of a ragged batch
+// (LIST false; ckv_q8_dense.cu) or a selected list per graph unit (LIST true;
+// ckv_q8_sparse.cu).  The tile arithmetic and what bounds it: ckv_q8_attend.cuh.
+//
+// Work split: a unit (a KV head of a request; a graph unit with its list) is
+// ceil(tokens / TOK) tiles; each block has one range of tiles, found by every
+// block for itself from the lengths.
+// Where pieces of about an equal share that do not cross units are no more than
+// the blocks, each block has one piece, and so one start and one join; otherwise
+// the units are laid end to end and cut into equal ranges, which may cross units.
+// The second way costs a block that crosses a unit about 12 tiles' time (a new
+// query, an empty ring, a join), the first the difference between the longest
+// piece and the share: the smaller loss decides.  (Finer pieces by ticket, for the
+// SMs' 10 % difference in bandwidth, lost more by their starts: 8 requests of
+// 128K tokens 357 against 350 us, 8 heads a group at 64K 249 against 200.)
+//
+// Inside a segment of a unit the warps take tiles in turn, each with its own ring of
+// staged tiles and its own softmax state, joined in shared memory.  A unit that
+// one block holds whole is finished there; otherwise the blocks write partials
+// and the last one to arrive (a counter per unit, returned to zero) joins them in
+// order: the result does not depend on which block that is, no block waits for
+// another, and the whole call is one launch.
+//
+// A list entry's position goes through the request's block table, a window of 32
+// entries ahead of the copies, and each row brings its own two scales.
+#pragma once
+
+#include "ckv_q8_attend.cuh"
+
+namespace ckv {
+
+constexpr int QD_WARPS = 4;
+constexpr int QD_THREADS = QD_WARPS * 32;
+constexpr int QD_MAX_GRID = 640;    // >= resident blocks
+constexpr int QD_WHOLE = 12;        // tiles: a unit up to this long stays whole
+constexpr int QD_MIN_PIECE = 8;     // tiles: least piece of a longer one; shorter ones cost more to join than they save
+constexpr int QD_CROSS = 12;        // tiles: what crossing a unit costs a block
+
+// Rows in order: tiles of two halves, 12 warps an SM.  Lists, which wait longer for
+// scattered rows: one half, 16 warps.
+template <int D, bool LIST>
+struct QdShape {
+    static constexpr int NH = LIST ? 1 : 2;
+    static constexpr int TOK = NH * Q8_HALF;              // tokens of a tile
+    static constexpr int CTAS = LIST ? 4 : 3;             // resident blocks per SM
+    static constexpr int STAGES = LIST ? (D == 128 ? 3 : 5) : (D == 128 ? 2 : 4);
+};
+
+struct BlocksQ8Params {
+    Q8View c;
+    const void* q;
+    float* out;
+    float scale_log2;
+    // LIST: U units, G per request
+    int U, G, per_head, tok_cap;
+    const int32_t* sel_tok;
+    const int32_t* n_tok;
+    int* count;   // [units], zero between calls
+    float* m;     // partials: two slots a block
+    float* l;
+    float* acc;
+};
+
+template <int D, int GQ, bool LIST>
+struct BlocksQ8Smem {
+    static constexpr int WARP = QdShape<D, LIST>::STAGES * Q8Geom<D, QdShape<D, LIST>::NH>::SLOT;  // a warp's ring, then its accumulators
+    static constexpr int FIXED = QD_WARPS * WARP + 2 * QD_WARPS * GQ * 4;
+    static_assert(GQ * D * 4 <= WARP, "a warp's accumulators fit its ring");
+    // the join of a unit's partials: weights and sums of JOIN slots at a time
+    static constexpr int JOIN = 128;
+    static_assert(2 * JOIN * GQ * 4 + QD_THREADS * 16 <= QD_WARPS * WARP, "the join fits the rings");
+};
+
+// Joins the partials of a unit that blocks c0 .. c0 + np - 1 share into out, JOIN
+// at a time.  A block's first segment has its even slot, its last (when that is
+// another) the odd one: `odd` for block c0.  References
+// and sums first, all at once, then the weighted rows with the slots shared out
+// over the threads.
+template <int D, int GQ, bool LIST>
+__device__ __forceinline__ void join_partials(const BlocksQ8Params& p, int c0, int np, int odd, float* out,
+                                              unsigned char* smem, float* s_head, int tid) {
+    constexpr int JOIN = BlocksQ8Smem<D, GQ, LIST>::JOIN;
+    constexpr int VECS = GQ * D / 4;  // float4 of an output
+    constexpr int SHARE = QD_THREADS / VECS > 0 ? QD_THREADS / VECS : 1;      // threads to a float4
+    constexpr int PER = SHARE > 1 ? 1 : (VECS + QD_THREADS - 1) / QD_THREADS;  // float4 to a thread
+    const int lane = tid & 31, warp = tid >> 5;
+    float* s_f = reinterpret_cast<float*>(smem);  // [JOIN][GQ] references, then weights
+    float* s_l = s_f + JOIN * GQ;                 // [JOIN][GQ] sums
+    float4* s_part = reinterpret_cast<float4*>(s_l + JOIN * GQ);
+    float* s_m = s_head;                          // [GQ] running reference, sum and the old rows' factor
+    float* s_sum = s_head + GQ;
+    __shared__ float s_old[GQ];
+    if (tid < GQ) {
+        s_m[tid] = Q8_M_INIT;
+        s_sum[tid] = 0.f;
+    }
+    const int part = SHARE > 1 ? tid / VECS : 0, x0 = SHARE > 1 ? tid % VECS : tid;
+    float4 A[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) A[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < np; i0 += JOIN) {
+        const int n = min(np - i0, JOIN);
+        __syncthreads();
+        auto slot_of = [&](int i) { return 2 * (c0 + i0 + i) + (i0 + i == 0 ? odd : 0); };
+        for (int x = tid; x < n * GQ; x += QD_THREADS) {
+            const int at = slot_of(x / GQ) * GQ + x % GQ;
+            s_f[x] = __ldcg(p.m + at);
+            s_l[x] = __ldcg(p.l + at);
+        }
+        __syncthreads();
+        for (int h = warp; h < GQ; h += QD_WARPS) {
+            float M = s_m[h], L = 0.f;
+            const float before = M;
+            for (int i = lane; i < n; i += 32) M = fmaxf(M, s_f[i * GQ + h]);
+#pragma unroll
+            for (int k = 16; k >= 1; k >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, k));
+            for (int i = lane; i < n; i += 32) {
+                const float f = exp2_approx(s_f[i * GQ + h] - M);
+                s_f[i * GQ + h] = f;
+                L = fmaf(s_l[i * GQ + h], f, L);
+            }
+#pragma unroll
+            for (int k = 16; k >= 1; k >>= 1) L += __shfl_xor_sync(FULL, L, k);
+            if (lane == 0) {
+                const float f = exp2_approx(before - M);
+                s_old[h] = f;
+                s_m[h] = M;
+                s_sum[h] = fmaf(s_sum[h], f, L);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int x = x0 + k * QD_THREADS, h = x / (D / 4);
+            if (x >= VECS || part >= SHARE) continue;
+            const float4* acc = reinterpret_cast<const float4*>(p.acc) + x;
+            const float fo = s_old[h];
+            A[k].x *= fo;
+            A[k].y *= fo;
+            A[k].z *= fo;
+            A[k].w *= fo;
+#pragma unroll 16
+            for (int i = part; i < n; i += SHARE) {
+                const float4 v = __ldcg(acc + (size_t)slot_of(i) * VECS);
+                const float f = s_f[i * GQ + h];
+                A[k].x = fmaf(v.x, f, A[k].x);
+                A[k].y = fmaf(v.y, f, A[k].y);
+                A[k].z = fmaf(v.z, f, A[k].z);
+                A[k].w = fmaf(v.w, f, A[k].w);
+            }
+        }
+    }
+    if constexpr (SHARE > 1) {
+        s_part[tid] = A[0];
+        __syncthreads();
+        if (part == 0) {
+#pragma unroll
+            for (int k = 1; k < SHARE; ++k) {
+                const float4 v = s_part[k * VECS + tid];
+                A[0].x += v.x;
+                A[0].y += v.y;
+                A[0].z += v.z;
+                A[0].w += v.w;
+            }
+        }
+    }
+    if (part == 0) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int x = x0 + k * QD_THREADS;
+            if (x >= VECS) continue;
+            const float L = s_sum[x / (D / 4)];
+            const float inv = L == 0.f ? 0.f : 1.f / L;  // no weight: every block of the unit was out of range
+            reinterpret_cast<float4*>(out)[x] = make_float4(A[k].x * inv, A[k].y * inv, A[k].z * inv, A[k].w * inv);
+        }
+    }
+}
+
+// 16 whole rows of K and of V, each 16 D contiguous bytes (k, v: lane's first 16 of
+// them), to sm + SO.  Rows 4 apart (d = 128) differ in the swizzle by one bit.
+template <int D, int SO>
+__device__ __forceinline__ void copy_half(unsigned sm, const char* k, const char* v, int lane) {
+    constexpr int V = Q8Geom<D, 2>::V + SO;
+    const unsigned even = sm + q8_swz<D>(lane / Q8Geom<D, 2>::CH, lane % Q8Geom<D, 2>::CH);
+    cp_async_16i<SO, 0>(even, k);
+    cp_async_16i<V, 0>(even, v);
+    if constexpr (D == 128) {
+        const unsigned odd = sm + (q8_swz<D>(lane / 8, lane % 8) ^ 64);
+        cp_async_16i<SO + 512, 512>(odd, k);
+        cp_async_16i<SO + 1024, 1024>(even, k);
+        cp_async_16i<SO + 1536, 1536>(odd, k);
+        cp_async_16i<V + 512, 512>(odd, v);
+        cp_async_16i<V + 1024, 1024>(even, v);
+        cp_async_16i<V + 1536, 1536>(odd, v);
+    } else {
+        cp_async_16i<SO + 512, 512>(even, k);
+        cp_async_16i<V + 512, 512>(even, v);
+    }
+}
+
+template <int D, int GQ, int FMT, bool LIST>
+__global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_kernel(const __grid_constant__ BlocksQ8Params p) {
+    using SH = QdShape<D, LIST>;
+    using QG = Q8Geom<D, SH::NH>;
+    using W = Q8Warp<D, GQ, FMT, SH::NH>;
+    using SM = BlocksQ8Smem<D, GQ, LIST>;
+    constexpr int STAGES = SH::STAGES, TOK = SH::TOK;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ int s_last;
+    const TableView& t = p.c.t;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // groups of units of one length: requests with Hkv units each, or single lists
+    const int B = LIST ? p.U : t.B, H = LIST ? 1 : p.c.Hkv;
+    const int Hkv = p.c.Hkv, bs = t.block, grid = gridDim.x;
+    unsigned char* ring = smem + warp * SM::WARP;
+    float* wm = reinterpret_cast<float*>(smem + QD_WARPS * SM::WARP);  // [warps][GQ]
+    float* wl = wm + QD_WARPS * GQ;
+    int* s_nt = reinterpret_cast<int*>(smem + SM::FIXED);              // [B] tiles of a unit of group b
+    pdl_wait();
+
+    for (int b = tid; b < B; b += QD_THREADS) {
+        int n;
+        if constexpr (LIST) {
+            n = max(0, min(p.n_tok[b], p.tok_cap));
+        } else {
+            n = t.len[b];
+            if (n < 0 || n > (long long)t.max_blocks * bs) {
+                if (blockIdx.x == 0) atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
+                n = 0;
+            }
+        }
+        s_nt[b] = (n + TOK - 1) / TOK;
+    }
+    __syncthreads();
+    // from here every warp works for itself, 32 groups at a time
+    auto ceil_div = [](int a, int b) { return (int)(((unsigned)a + b - 1) / (unsigned)b); };
+    auto pieces = [&](int nt, int piece) { return nt <= QD_WHOLE ? min(nt, 1) : ceil_div(nt, piece); };
+    auto sum_over = [&](auto f) {
+        int own = 0;
+        for (int b = lane; b < B; b += 32) own += f(s_nt[b]);
+        return __reduce_add_sync(FULL, own);
+    };
+    const int total = sum_over([](int nt) { return nt; }) * H;
+    if (total == 0) {
+        for (int i = blockIdx.x * QD_THREADS + tid; i < t.B * p.c.Hq * D; i += grid * QD_THREADS) p.out[i] = 0.f;
+        return;
+    }
+    const int share = ceil_div(total, grid);
+    // pieces of at most `piece` tiles: 0 where the units are laid end to end instead
+    const int per = max(share, QD_MIN_PIECE);
+    const int most = per + max(QD_CROSS, share >> 4);
+    int piece = per, items = 0;
+    while (true) {
+        items = sum_over([&](int nt) { return pieces(nt, piece); }) * H;
+        if (items <= grid) break;
+        if (piece >= most || B * H > 2 * grid) {
+            piece = 0;
+            break;
+        }
+        piece = min(piece + max(1, (most - per) >> 2), most);
+    }
+    // [start, end): this block's range, in pieces or in tiles
+    const int start = piece ? (int)blockIdx.x : (int)min((long long)blockIdx.x * per, (long long)total);
+    const int end = piece ? min(start + 1, items) : min(start + per, total);
+    // The query rows of a unit: in LIST mode group b is graph unit b, and `kvh` its KV head
+    auto first_row = [&](int b, int h, int& kvh) {
+        if constexpr (LIST) {
+            const int s = b / p.G, g = b - s * p.G;
+            kvh = p.per_head ? g / (p.c.Hq / Hkv) : g;
+            return (size_t)s * p.c.Hq + g * GQ;
+        } else {
+            kvh = h;
+            return (size_t)b * p.c.Hq + h * GQ;
+        }
+    };
+    for (int b = blockIdx.x; b < B; b += grid)
+        if (s_nt[b] == 0) {  // nothing to attend to
+            int kvh;
+            float* o = p.out + first_row(b, 0, kvh) * D;
+            for (int i = tid; i < H * GQ * D; i += QD_THREADS) o[i] = 0.f;
+        }
+
+    W st;
+    for (int at = start; at < end;) {
+        // the segment: tiles [lo, hi) of unit h of group b, the unit shared by the blocks c0 .. c0 + np - 1
+        int b = 0, pre = 0;  // pre: what comes before group b
+        for (int k = 0;; k += 32) {
+            const int x = k + lane < B ? s_nt[k + lane] : 0;
+            int own = (piece ? pieces(x, piece) : x) * H, inc = own;
+#pragma unroll
+            for (int y = 1; y < 32; y <<= 1) {
+                const int z = __shfl_up_sync(FULL, inc, y);
+                if (lane >= y) inc += z;
+            }
+            const int chunk = __shfl_sync(FULL, inc, 31);
+            if (at < pre + chunk) {  // the first group that ends past `at`
+                const int l = __ffs(__ballot_sync(FULL, at < pre + inc)) - 1;
+                b = k + l;
+                pre += __shfl_sync(FULL, inc - own, l);
+                break;
+            }
+            pre += chunk;
+        }
+        const int nt = s_nt[b];
+        int h, lo, hi, c0, np, odd = 0, slot = 2 * blockIdx.x;
+        if (piece) {
+            np = pieces(nt, piece);
+            h = (at - pre) / np;
+            const int i = (at - pre) - h * np;
+            lo = (int)((long long)nt * i / np);
+            hi = (int)((long long)nt * (i + 1) / np);
+            c0 = blockIdx.x - i;
+            at = end;
+        } else {
+            h = (at - pre) / nt;
+            const int ubeg = pre + h * nt;
+            lo = at - ubeg;
+            hi = min(end - ubeg, nt);
+            c0 = ubeg / per;
+            np = (ubeg + nt - 1) / per - c0 + 1;
+            odd = ubeg - c0 * per != 0 ? 1 : 0;
+            slot += at == start ? 0 : 1;
+            at = ubeg + hi;
+        }
+        int kvh;
+        const size_t row0 = first_row(b, h, kvh);
+        const auto raw_q = W::fetch_q(W::q_row(p.q, p.c.dtype, row0), p.c.dtype, lane);
+        const int seq = LIST ? b / p.G : b;
+        const int32_t* table = t.table + (size_t)seq * t.max_blocks;
+        // n: the unit's tokens (list entries)
+        const int n = LIST ? max(0, min(p.n_tok[b], p.tok_cap)) : t.len[b];
+
+        const int nit = (hi - lo - warp + QD_WARPS - 1) / QD_WARPS;  // this warp's tiles: lo + warp + QD_WARPS i
+        const unsigned ring32 = smem_addr32(ring);
+        unsigned stage_in = 0;
+        // a window of 16 tiles: lane 2 i + j holds the block of half j of this warp's tile i
+        auto rows_block = [&](int x) {
+            const int pos = (lo + warp + QD_WARPS * (x + (lane >> 1))) * TOK + (lane & 1) * Q8_HALF;
+            return x + (lane >> 1) < nit && pos < n ? table[pos >> t.sh] : 0;
+        };
+        int win_cur = 0, win_nxt = 0;
+        if constexpr (!LIST) {
+            win_cur = rows_block(0);
+            win_nxt = rows_block(16);
+        }
+        const char* klane = static_cast<const char*>(p.c.k) + lane * 16;
+        const char* vlane = static_cast<const char*>(p.c.v) + lane * 16;
+        const float* slane = lane < 2 ? p.c.k_scale : p.c.v_scale;  // lanes 0..3 copy the halves' scales
+        unsigned bad = 0;  // bit 2 s + j: the block of half j of the tile in ring slot s is out of range
+        auto issue_rows = [&](int x) {
+            if (x < nit) {
+                if ((x & 15) == 0 && x > 0) {
+                    win_cur = win_nxt;
+                    win_nxt = rows_block(x + 16);
+                }
+                const unsigned sm = ring32 + stage_in * QG::SLOT;
+                const int id0 = __shfl_sync(FULL, win_cur, 2 * (x & 15)), id1 = __shfl_sync(FULL, win_cur, 2 * (x & 15) + 1);
+                const int pos = (lo + warp + QD_WARPS * x) * TOK;
+                const bool ok0 = (unsigned)id0 < (unsigned)t.n_blocks, ok1 = (unsigned)id1 < (unsigned)t.n_blocks;
+                const unsigned unit0 = id0 * Hkv + h, unit1 = id1 * Hkv + kvh;
+                const size_t src0 = (size_t)((unit0 << t.sh) + (pos & (bs - 1))) * D;
+                const size_t src1 = (size_t)((unit1 << t.sh) + ((pos + Q8_HALF) & (bs - 1))) * D;
+                if (pos + TOK <= n && ok0 && ok1) {
+                    copy_half<D, 0>(sm, klane + src0, vlane + src0, lane);
+                    copy_half<D, Q8Geom<D, 2>::HALF>(sm, klane + src1, vlane + src1, lane);
+                    bad &= ~(3u << 2 * stage_in);
+                    cp_async_4p(sm + QG::SCALES + 8 * (lane & 1) + 4 * (lane >> 1), slane + (lane & 1 ? unit1 : unit0), lane < 4);
+                } else {
+                    // the end of the request, or a block out of range: zeros where there is nothing
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const bool ok = j ? ok1 : ok0;
+                        const size_t src = ok ? (j ? src1 : src0) : 0;
+                        const int rows = ok ? n - pos - j * Q8_HALF : 0;
+#pragma unroll
+                        for (int y = 0; y < QG::HALF / 512; ++y) {
+                            const int idx = y * 32 + lane, row = idx / QG::CH, c = idx % QG::CH;
+                            const unsigned dst = sm + j * QG::HALF + q8_swz<D>(row, c);
+                            const int size = row < rows ? 16 : 0;
+                            const size_t from = size ? src + y * 512 : 0;
+                            cp_async_16s(dst, klane + from, size);
+                            cp_async_16s(dst + QG::V, vlane + from, size);
+                        }
+                        if (lane < 2)
+                            cp_async_4s(sm + QG::SCALES + 8 * j + 4 * lane,
+                                        (lane ? p.c.v_scale : p.c.k_scale) + (rows > 0 ? (j ? unit1 : unit0) : 0),
+                                        rows > 0 ? 4 : 0);
+                    }
+                    bad = (bad & ~(3u << 2 * stage_in)) | ((ok0 ? 0u : 1u) | (ok1 ? 0u : 2u)) << 2 * stage_in;
+                    if (lane == 0 && !(ok0 && ok1)) atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
+                }
+            }
+            stage_in = stage_in + 1 == STAGES ? 0 : stage_in + 1;
+            cp_async_commit();
+        };
+        // Two tiles' entries of this warp are a window, one entry a lane.  The copies of
+        // a window need its positions and their blocks: loaded two and one windows ahead,
+        // and only looked at by the copies themselves, so that no load is waited for
+        // where it is issued.
+        const int len = LIST ? (int)max(0ll, min((long long)t.len[seq], (long long)t.max_blocks << t.sh)) : 0;
+        const int32_t* toks = LIST ? p.sel_tok + (size_t)b * p.tok_cap : nullptr;
+        auto entry = [&](int w) {  // of this lane in window w
+            return (lo + warp + QD_WARPS * (2 * w + (lane >> 4))) * TOK + (lane & 15);
+        };
+        auto position = [&](int w) { return 2 * w + (lane >> 4) < nit && entry(w) < n ? toks[entry(w)] : -1; };
+        auto inside = [&](int pos) { return pos >= 0 && pos < len; };
+        auto list_block = [&](int pos) { return inside(pos) ? table[pos >> t.sh] : -1; };
+        int pos0 = 0, pos1 = 0, id0 = 0, row_cur = -1;  // row_cur: the entry's row of the pool; -1: not attended
+        // the tiles' scales (lanes 0..15 K's, 16..31 V's) and masks, newest first
+        float scales[STAGES];
+        unsigned masks[STAGES];
+        const float* lscale = lane < 16 ? p.c.k_scale : p.c.v_scale;
+        if constexpr (LIST) {
+            pos0 = position(0);
+            pos1 = position(1);
+            id0 = list_block(pos0);
+        }
+        auto issue_list = [&](int x) {
+#pragma unroll
+            for (int k = STAGES - 1; k > 0; --k) {
+                scales[k] = scales[k - 1];
+                masks[k] = masks[k - 1];
+            }
+            if (x < nit) {
+                if ((x & 1) == 0) {
+                    row_cur = -1;
+                    if (inside(pos0) && (unsigned)id0 < (unsigned)t.n_blocks)
+                        row_cur = ((id0 * Hkv + kvh) << t.sh) + (pos0 & (bs - 1));
+                    else if (x + (lane >> 4) < nit && entry(x >> 1) < n)
+                        atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
+                    pos0 = pos1;
+                    id0 = list_block(pos0);
+                    pos1 = position((x >> 1) + 2);
+                }
+                const unsigned sm = ring32 + stage_in * QG::SLOT;
+                const int base = (x & 1) << 4;
+                const int mine = __shfl_sync(FULL, row_cur, base + (lane & 15));
+                scales[0] = mine >= 0 ? lscale[mine >> t.sh] : 0.f;
+                masks[0] = __ballot_sync(FULL, mine >= 0) & 0xffffu;
+#pragma unroll
+                for (int y = 0; y < QG::HALF / 512; ++y) {
+                    const int idx = y * 32 + lane, r = idx / QG::CH, c = idx % QG::CH;
+                    const int row = __shfl_sync(FULL, row_cur, base + r);
+                    const int size = row >= 0 ? 16 : 0;
+                    const size_t src = (size_t)max(row, 0) * D + c * 16;
+                    const unsigned dst = sm + q8_swz<D>(r, c);
+                    cp_async_16s(dst, static_cast<const char*>(p.c.k) + src, size);
+                    cp_async_16s(dst + QG::V, static_cast<const char*>(p.c.v) + src, size);
+                }
+            }
+            stage_in = stage_in + 1 == STAGES ? 0 : stage_in + 1;
+            cp_async_commit();
+        };
+        auto issue = [&](int x) {
+            if constexpr (LIST) issue_list(x);
+            else issue_rows(x);
+        };
+#pragma unroll
+        for (int x = 0; x < STAGES - 1; ++x) issue(x);
+        st.set_q(raw_q, p.c.dtype, p.scale_log2, lane);
+        st.reset();
+        unsigned stage_out = 0;
+        int left = n - (lo + warp) * TOK;  // tokens from this tile's first on
+        for (int x = 0; x < nit; ++x) {
+            __syncwarp();  // every lane is done reading the slot refilled next
+            issue(x + STAGES - 1);
+            cp_async_wait<STAGES - 1>();
+            __syncwarp();  // what the other lanes copied is visible
+            unsigned mask;
+            if constexpr (LIST) {
+                mask = masks[STAGES - 1];
+            } else {
+                mask = 0xffffffffu;
+                if (left < TOK) mask >>= TOK - left;
+                if (bad) mask &= ~((bad >> 2 * stage_out & 1u) * 0xffffu | (bad >> 2 * stage_out & 2u) * 0x7fff8000u);
+                left -= QD_WARPS * TOK;
+            }
+            st.template tile<!LIST, false>(ring32 + stage_out * QG::SLOT, mask, LIST ? scales[STAGES - 1] : 0.f, lane,
+                                           [](int, float) {});
+            stage_out = stage_out + 1 == STAGES ? 0 : stage_out + 1;
+        }
+        cp_async_wait<0>();
+        __syncwarp();
+        // the warps' states through their rings' memory
+        st.write(wm + warp * GQ, wl + warp * GQ, reinterpret_cast<float*>(ring), lane);
+        __syncthreads();
+        float* out = p.out + row0 * D;
+        for (int x = tid; x < GQ * D; x += QD_THREADS) {
+            const int hh = x / D;
+            float M = Q8_M_INIT;
+#pragma unroll
+            for (int w = 0; w < QD_WARPS; ++w) M = fmaxf(M, wm[w * GQ + hh]);
+            float L = 0.f, A = 0.f;
+#pragma unroll
+            for (int w = 0; w < QD_WARPS; ++w) {
+                const float f = exp2_approx(wm[w * GQ + hh] - M);
+                L = fmaf(wl[w * GQ + hh], f, L);
+                A = fmaf(reinterpret_cast<const float*>(smem + w * SM::WARP)[x], f, A);
+            }
+            if (np == 1) {
+                out[x] = L == 0.f ? 0.f : A / L;  // no weight: every block of the unit was out of range
+            } else {
+                p.acc[(size_t)slot * GQ * D + x] = A;
+                if (x % D == 0) {
+                    p.m[slot * GQ + hh] = M;
+                    p.l[slot * GQ + hh] = L;
+                }
+            }
+        }
+        if (np > 1) {
+            const int unit = b * H + h;
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                s_last = atomicAdd(p.count + unit, 1) == np - 1;
+                if (s_last) p.count[unit] = 0;
+            }
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                join_partials<D, GQ, LIST>(p, c0, np, odd, out, smem, wm, tid);
+            }
+        }
+        __syncthreads();  // the rings are free again
+    }
+}
+
+// Resident blocks, but no more than there can be pieces (`tiles`: the most the units can have).
+template <int D, int GQ, int FMT, bool LIST>
+static cudaError_t launch_blocks_q8_t(const BlocksQ8Params& p, long long tiles, cudaStream_t st) {
+    static LaunchCache lc;
+    auto kern = blocks_q8_kernel<D, GQ, FMT, LIST>;
+    const size_t smem = BlocksQ8Smem<D, GQ, LIST>::FIXED + (size_t)(LIST ? p.U : p.c.t.B) * 4;
+    int per_sm = 0, sms = 0;
+    cudaError_t e = prepare_launch(kern, lc, smem, QD_THREADS, &per_sm, &sms);
+    if (e != cudaSuccess) return e;
+    if (sms <= 0 || per_sm <= 0) return cudaErrorInvalidConfiguration;
+    const int grid = (int)min((long long)min(sms * per_sm, QD_MAX_GRID), tiles);
+    return launch_pdl(KK_ATTENTION, kern, dim3(grid), dim3(QD_THREADS), smem, st, p);
+}
+
+// The workspace's parts after its head: the units' counters, then the partials.
+inline void carve_blocks_ws(BlocksQ8Params& p, void* ws, int gq, int counters) {
+    char* w = static_cast<char*>(ws) + WS_RESERVED;
+    p.count = reinterpret_cast<int*>(w);
+    w += q8_counter_bytes(counters);
+    p.m = reinterpret_cast<float*>(w);
+    w += align256((size_t)2 * QD_MAX_GRID * gq * 4);
+    p.l = reinterpret_cast<float*>(w);
+    w += align256((size_t)2 * QD_MAX_GRID * gq * 4);
+    p.acc = reinterpret_cast<float*>(w);
+}
+
+}  // namespace ckv

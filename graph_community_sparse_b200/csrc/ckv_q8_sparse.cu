@@ -5,13 +5,15 @@
 // re-clustering", paragraphs 4-5), read in place from a cache in 8 bits.  The
 // tile arithmetic and what bounds it: ckv_q8_attend.cuh.
 //
-// The split over warps (equal slices of the concatenated lists, then chunks by
-// ticket) and the merge kernel with its neighbour search and fused update are those
-// of the 16/32-bit cache's attention (ckv_decode.cuh).  What differs is the way
-// to a row: a list entry's position goes through the request's block table,
-// one window of 32 entries ahead of the copies, and each row brings its own two
-// scales (the blocks' scales of a request fit L1 or L2 and are read many times).
-#include "ckv_q8_attend.cuh"
+// Without neighbours to find, one launch of the block-split kernel
+// (ckv_q8_blocks.cuh).  With them, two: the graph logits of the whole list have to
+// be there before the search, so the split over warps (equal slices of the
+// concatenated lists, then chunks by ticket) and the merge kernel with its
+// neighbour search and fused update are those of the 16/32-bit cache's attention
+// (ckv_decode.cuh).  What differs is the way to a row: a list entry's position goes
+// through the request's block table, one window of 32 entries ahead of the copies,
+// and each row brings its own two scales.
+#include "ckv_q8_blocks.cuh"
 
 namespace ckv {
 
@@ -227,7 +229,7 @@ cudaError_t launch_sparse_decode_q8(const Q8View& c, const GraphView& g, const S
     d.unit_prefix = s.unit_prefix;
     d.n_tok = s.n_tok;
     d.scale_log2 = 1.4426950408889634f / sqrtf((float)c.d);
-    d.ws = carve_decode_ws(ws, WS_RESERVED + q8_counter_bytes(c.t.B * c.Hkv), d.U, g.gq, c.d, s.tok_cap);
+    d.ws = carve_decode_ws(ws, WS_RESERVED + q8_counter_bytes(c.t.B * c.Hq), d.U, g.gq, c.d, s.tok_cap);
     d.want_nbr = nbr8 != nullptr || k_new != nullptr;
     d.out = out;
     d.nbr8 = nbr8;
@@ -245,6 +247,29 @@ cudaError_t launch_sparse_decode_q8(const Q8View& c, const GraphView& g, const S
         d.ap.k = k_new;  // nothing is written to a cache here: k_dst stays NULL
         d.ap.sb = (int64_t)c.Hkv * c.d;
         d.ap.sh = c.d;
+    }
+    if (!d.want_nbr) {
+        BlocksQ8Params b{};
+        b.c = c;
+        b.q = q;
+        b.out = out;
+        b.scale_log2 = d.scale_log2;
+        b.U = d.U;
+        b.G = d.G;
+        b.per_head = d.per_head;
+        b.tok_cap = d.tok_cap;
+        b.sel_tok = d.sel_tok;
+        b.n_tok = d.n_tok;
+        carve_blocks_ws(b, ws, g.gq, c.t.B * c.Hq);
+        const long long tiles = (long long)d.U * (d.tok_cap / (QD_MIN_PIECE * 16) + 1);
+#define CKV_QL(DD, GG)                                                                  \
+        if (c.d == DD && g.gq == GG)                                                    \
+            return c.format == Q8_I8 ? launch_blocks_q8_t<DD, GG, Q8_I8, true>(b, tiles, st) \
+                                     : launch_blocks_q8_t<DD, GG, Q8_E4, true>(b, tiles, st);
+        CKV_QL(64, 1) CKV_QL(64, 2) CKV_QL(64, 4) CKV_QL(64, 8)
+        CKV_QL(128, 1) CKV_QL(128, 2) CKV_QL(128, 4) CKV_QL(128, 8)
+#undef CKV_QL
+        return cudaErrorInvalidValue;
     }
 #define CKV_QS(DD, GG)             \
     if (c.d == DD && g.gq == GG)   \

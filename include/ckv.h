@@ -515,9 +515,9 @@ CKV_API ckv_status ckv_q8_read(const ckv_q8_desc* cache, const int32_t* first, i
 
 /*
  * Workspace of the two attention calls below (graph and sel NULL: the dense
- * one alone).  Unlike the other calls' it keeps a counter per (request, KV head):
+ * one alone).  Unlike the other calls' it keeps a counter per (request, query head):
  * zero-fill the whole workspace once after allocating it, and give it to these
- * two calls only, with the B and Hkv that it was sized for; every call leaves the
+ * two calls only, with the B and Hq that it was sized for; every call leaves the
  * counters zero.  Calls sharing it must not overlap on the GPU (graphs captured
  * with one workspace included).
  */
