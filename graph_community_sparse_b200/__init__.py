@@ -522,6 +522,13 @@ class BlockTable:
     n_free: Optional[torch.Tensor]     # int32 [1]
     dev_err: torch.Tensor    # int32 [1]
 
+    def __post_init__(self):
+        self.device, self.shape, self.ref_blocks = self.len.device, self.len.shape, ctypes.byref(self.desc)
+
+    @property
+    def blocks(self) -> "BlockTable":
+        return self
+
 
 @dataclass
 class Q8Cache:
@@ -533,6 +540,14 @@ class Q8Cache:
     k_scale: torch.Tensor    # fp32 [n_blocks, Hkv]
     v_scale: torch.Tensor
     dtype: torch.dtype
+
+    def __post_init__(self):
+        # what every call looks at, read once: a decode step's calls are a few
+        # microseconds each on the host
+        c = self.desc
+        self.B, self.Hkv, self.Hq, self.d, self.device = c.blocks.B, c.Hkv, c.Hq, c.d, self.k.device
+        self.q_shape, self.row_shape = torch.Size((self.B, self.Hq, self.d)), torch.Size((self.B, self.Hkv, self.d))
+        self.ref, self.ref_blocks = ctypes.byref(c), ctypes.byref(self.blocks.desc)
 
     @property
     def dev_err(self) -> torch.Tensor:
@@ -556,9 +571,11 @@ class Plan:
 
     def __post_init__(self):
         B, dev = self.granted.shape[0], self.granted.device
+        self.n_rows, self.device, self.shape = self.slot.numel(), dev, self.granted.shape
         self.desc = PlanDesc(self.slot.numel(), _need("start", self.start, torch.int32, (B + 1,), dev),
                              _need("slot", self.slot, torch.int32, (self.slot.numel(),), dev),
                              _need("granted", self.granted, torch.int32, (B,), dev))
+        self.ref = ctypes.byref(self.desc)
 
 
 def block_table(table: torch.Tensor, length: torch.Tensor, free_list: Optional[torch.Tensor],
@@ -634,43 +651,47 @@ def q8_shape(cache: Q8Cache, T_cap: int) -> CacheDesc:
     return CacheDesc(c.dtype, c.blocks.B, c.Hkv, c.Hq, c.d, T_cap, None, None, 0, 0, 0)
 
 
-def _of_plan(cache, plan: Plan) -> None:
-    if plan.granted.shape[0] != cache.len.shape[0] or plan.granted.device != cache.len.device:
+def _of_plan(blocks: BlockTable, plan: Plan) -> None:
+    if plan.shape != blocks.shape or plan.device != blocks.device:
         raise ValueError("the plan was made for another batch size or device")
 
 
 def ckv_plan_blocks(cache, add: torch.Tensor, plan: Plan, stream=None) -> None:
     """Request b of a BlockTable or Q8Cache changes by add[b] tokens (int32 [B])."""
-    bt = cache.blocks if isinstance(cache, Q8Cache) else cache
+    bt = cache.blocks
     _of_plan(bt, plan)
-    dev = bt.len.device
-    _call("ckv_plan_blocks", lib.ckv_plan_blocks, dev, stream, ctypes.byref(bt.desc),
-          _need("add", add, torch.int32, bt.len.shape, dev), ctypes.byref(plan.desc))
+    _call("ckv_plan_blocks", lib.ckv_plan_blocks, bt.device, stream, bt.ref_blocks,
+          _need("add", add, torch.int32, bt.shape, bt.device), plan.ref)
+
+
+def _rows(cache: Q8Cache, names, k: torch.Tensor, v: torch.Tensor, shape):
+    """The common strides of a pair of row tensors of this shape."""
+    strides, dtype, dev = k.stride(), cache.dtype, cache.device
+    if (k.shape != shape or v.shape != shape or k.dtype is not dtype or v.dtype is not dtype or k.device != dev
+            or v.device != dev or v.stride() != strides or strides[-1] != 1):
+        raise ValueError(f"{names} must be {dtype} tensors of shape {tuple(shape)} on {dev} with contiguous rows and common "
+                         f"strides, got {k.dtype} {tuple(k.shape)} {strides} on {k.device} and {v.dtype} "
+                         f"{tuple(v.shape)} {v.stride()} on {v.device}")
+    return strides
 
 
 def ckv_quant_append(cache: Q8Cache, plan: Plan, k_new: torch.Tensor, v_new: torch.Tensor, stream=None) -> None:
     """k_new, v_new: packed rows [n_rows, Hkv, d], or padded ones [B, T, Hkv, d]
     of which request b's first granted[b] count; cache dtype, any strides with
     contiguous rows of 16-byte multiples, the same for both."""
-    _of_plan(cache, plan)
-    c, dev = cache.desc, cache.k.device
-    n = plan.slot.numel()
+    _of_plan(cache.blocks, plan)
     if k_new.dim() == 3:
-        shape, T_rows = (n, c.Hkv, c.d), 0
+        T_rows = sb = 0
+        st, sh, _ = _rows(cache, "k_new and v_new", k_new, v_new, (plan.n_rows, cache.Hkv, cache.d))
     elif k_new.dim() == 4:
         T_rows = k_new.shape[1]
-        shape = (c.blocks.B, T_rows, c.Hkv, c.d)
+        sb, st, sh, _ = _rows(cache, "k_new and v_new", k_new, v_new, (cache.B, T_rows, cache.Hkv, cache.d))
     else:
         raise ValueError("k_new must be [n_rows, Hkv, d] or [B, T, Hkv, d]")
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if t.shape != shape or t.dtype != cache.dtype or t.device != dev or t.stride() != k_new.stride() or t.stride(-1) != 1:
-            raise ValueError(f"{name} must be a {cache.dtype} tensor of shape {shape} on {dev} with contiguous rows and "
-                             f"k_new's strides, got {t.dtype} {tuple(t.shape)} {t.stride()} on {t.device}")
-    if n == 0 or k_new.numel() == 0:
+    if plan.n_rows == 0 or k_new.numel() == 0:
         return
-    sb, st, sh = (0, k_new.stride(0), k_new.stride(1)) if T_rows == 0 else k_new.stride()[:3]
-    _call("ckv_quant_append", lib.ckv_quant_append, dev, stream, ctypes.byref(c), ctypes.byref(plan.desc),
-          k_new.data_ptr(), v_new.data_ptr(), T_rows, sb, st, sh)
+    _call("ckv_quant_append", lib.ckv_quant_append, cache.device, stream, cache.ref, plan.ref, k_new.data_ptr(),
+          v_new.data_ptr(), T_rows, sb, st, sh)
 
 
 def ckv_q8_read(cache: Q8Cache, k_out: torch.Tensor, v_out: torch.Tensor, first: Optional[torch.Tensor] = None,
@@ -678,18 +699,13 @@ def ckv_q8_read(cache: Q8Cache, k_out: torch.Tensor, v_out: torch.Tensor, first:
     """Fills k_out and v_out, [B, Hkv, R, d] in the cache dtype, with positions
     first[b] .. first[b] + R - 1 (first None: from 0); zeros past a request's
     end."""
-    c, dev = cache.desc, cache.k.device
     if k_out.dim() != 4:
         raise ValueError("k_out must be [B, Hkv, R, d]")
     R = k_out.shape[2]
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if (t.shape != (c.blocks.B, c.Hkv, R, c.d) or t.dtype != cache.dtype or t.device != dev
-                or t.stride() != k_out.stride() or t.stride(-1) != 1):
-            raise ValueError(f"{name} must be a {cache.dtype} [B, Hkv, R, d] tensor on {dev} with contiguous rows and "
-                             f"k_out's strides, got {t.dtype} {tuple(t.shape)} {t.stride()} on {t.device}")
-    at = None if first is None else _need("first", first, torch.int32, cache.len.shape, dev)
-    _call("ckv_q8_read", lib.ckv_q8_read, dev, stream, ctypes.byref(c), at, R, k_out.data_ptr(), v_out.data_ptr(),
-          k_out.stride(0), k_out.stride(1), k_out.stride(2))
+    sb, sh, st, _ = _rows(cache, "k_out and v_out", k_out, v_out, (cache.B, cache.Hkv, R, cache.d))
+    at = None if first is None else _need("first", first, torch.int32, cache.blocks.shape, cache.device)
+    _call("ckv_q8_read", lib.ckv_q8_read, cache.device, stream, cache.ref, at, R, k_out.data_ptr(), v_out.data_ptr(),
+          sb, sh, st)
 
 
 def ckv_q8_workspace_size(cache: Q8Cache, graph: Optional[Graph] = None, sel: Optional[Selection] = None) -> int:
@@ -701,17 +717,16 @@ def ckv_q8_workspace_size(cache: Q8Cache, graph: Optional[Graph] = None, sel: Op
 
 
 def _q8_attention(cache: Q8Cache, q: torch.Tensor, out: torch.Tensor, ws: torch.Tensor):
-    c, dev = cache.desc, cache.k.device
-    shape = (c.blocks.B, c.Hq, c.d)
+    dev = cache.device
     if ws.device != dev:
         raise ValueError("the workspace is on another device")
-    return dev, _need("q", q, cache.dtype, shape, dev), _need("out", out, torch.float32, shape, dev)
+    return _need("q", q, cache.dtype, cache.q_shape, dev), _need("out", out, torch.float32, cache.q_shape, dev)
 
 
 def ckv_dense_decode_q8(cache: Q8Cache, q: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """out [B, Hq, d] fp32: attention of q [B, Hq, d] over each request's tokens."""
-    dev, qp, op = _q8_attention(cache, q, out, ws)
-    _call("ckv_dense_decode_q8", lib.ckv_dense_decode_q8, dev, stream, ctypes.byref(cache.desc), qp, op, ws.data_ptr(),
+    qp, op = _q8_attention(cache, q, out, ws)
+    _call("ckv_dense_decode_q8", lib.ckv_dense_decode_q8, cache.device, stream, cache.ref, qp, op, ws.data_ptr(),
           ws.numel())
 
 
@@ -720,13 +735,13 @@ def ckv_sparse_decode_q8(cache: Q8Cache, q: torch.Tensor, graph: Graph, sel: Sel
                          assigned: Optional[torch.Tensor] = None, stream=None) -> None:
     """Attention over the selected positions; with k_new [B, Hkv, d] the new
     token also joins a community (ckv_sparse_decode_append without the rows)."""
-    dev, qp, op = _q8_attention(cache, q, out, ws)
-    c = cache.desc
-    if graph.dev_err.device != dev or sel.sel_tok.device != dev:
-        raise ValueError("the graph and the selection must be on the cache's device")
-    kp = None if k_new is None else _need("k_new", k_new, cache.dtype, (c.blocks.B, c.Hkv, c.d), dev)
-    U = graph.U
-    np_ = None if nbr8 is None else _need("nbr8", nbr8, torch.int32, (U, NEIGHBOURS), dev)
-    ap = None if assigned is None else _need("assigned", assigned, torch.int32, (U,), dev)
-    _call("ckv_sparse_decode_q8", lib.ckv_sparse_decode_q8, dev, stream, ctypes.byref(c), qp, ctypes.byref(graph.desc),
+    qp, op = _q8_attention(cache, q, out, ws)
+    dev = cache.device
+    U = cache.B * (cache.Hq if graph.desc.mode == PER_HEAD else cache.Hkv)
+    if graph.U != U or sel.n_tok.shape[0] != U or graph.dev_err.device != dev or sel.sel_tok.device != dev:
+        raise ValueError("the graph and the selection must be for this cache's batch and heads, on its device")
+    kp = None if k_new is None else _need("k_new", k_new, cache.dtype, cache.row_shape, dev)
+    np_ = None if nbr8 is None else _need("nbr8", nbr8, torch.int32, (graph.U, NEIGHBOURS), dev)
+    ap = None if assigned is None else _need("assigned", assigned, torch.int32, (graph.U,), dev)
+    _call("ckv_sparse_decode_q8", lib.ckv_sparse_decode_q8, dev, stream, cache.ref, qp, ctypes.byref(graph.desc),
           ctypes.byref(sel.desc), op, np_, kp, ap, ws.data_ptr(), ws.numel())

@@ -2,7 +2,8 @@
 
 ``LayerState`` owns (through PyTorch) the graph arrays, the selection and the
 workspace for one KV cache, and issues the four library calls in decode
-order.  It computes nothing itself.
+order.  ``PagedLayerState`` does the same over a paged 8-bit cache that requests
+of different lengths share.  They compute nothing themselves.
 """
 from __future__ import annotations
 
@@ -14,7 +15,9 @@ import torch
 from . import (ASSIGN_SCORE, ASSIGN_VOTE, PER_GROUP, PER_HEAD, Graph, Selection, cache_desc, ckv_append_assign, ckv_assign_update,
                ckv_sparse_decode_append,
                ckv_build_centroids, ckv_dense_decode, ckv_score_select, ckv_sparse_decode,
-               ckv_workspace_size, new_graph, new_selection, new_workspace, NEIGHBOURS)
+               ckv_workspace_size, new_graph, new_selection, new_workspace, NEIGHBOURS,
+               CacheDesc, Plan, Q8Cache, ckv_dense_decode_q8, ckv_plan_blocks, ckv_q8_read, ckv_q8_workspace_size,
+               ckv_quant_append, ckv_sparse_decode_q8, new_plan, q8_shape)
 
 
 @contextlib.contextmanager
@@ -119,3 +122,93 @@ class LayerState:
         with _range("ckv_dense_decode"):
             ckv_dense_decode(self.cache, q, self.T, out, self.ws, stream)
         return out
+
+
+class PagedLayerState:
+    """One layer's decode state over a paged 8-bit cache (`cache`, from
+    new_q8_cache) that up to cache.B requests share.
+
+    grow() takes slots for new tokens, or gives blocks back; write() quantises
+    the new tokens' rows into them; dense() attends to every token.  With Cmax > 0
+    it also holds community graphs over positions [0, T_cap): build(), select()
+    and attend() are LayerState's, over this cache.  A decode step with graphs is
+    select, attend (with the new keys, which join communities), grow, write.
+    """
+
+    def __init__(self, cache: Q8Cache, mode: str = "group", S: int = 0, Cmax: int = 0, max_tail: int = 0,
+                 T_cap: int = 0, tok_cap: Optional[int] = None, rule: str = "score"):
+        if rule not in ("score", "vote"):
+            raise ValueError(f"unknown assignment rule {rule!r}")
+        self.cache = cache
+        dev = cache.device
+        self.out = torch.empty(cache.q_shape, dtype=torch.float32, device=dev)
+        self.plan: Optional[Plan] = None
+        self._plans = {}  # by their number of rows: a decode step uses the same one again
+        self.graph = self.sel = None
+        if Cmax > 0:
+            self.shape: CacheDesc = q8_shape(cache, T_cap)
+            self.graph = new_graph(self.shape, PER_HEAD if mode == "head" else PER_GROUP, S, Cmax, max_tail, device=dev,
+                                   rule=ASSIGN_VOTE if rule == "vote" else ASSIGN_SCORE)
+            self.sel = new_selection(self.shape, self.graph, tok_cap or T_cap, device=dev)
+            self.nbr8 = torch.full((self.graph.U, NEIGHBOURS), -1, dtype=torch.int32, device=dev)
+            self.assigned = torch.full((self.graph.U,), -1, dtype=torch.int32, device=dev)
+            self.graph_ws = new_workspace(ckv_workspace_size(self.shape, self.graph, self.sel), device=dev)
+        self.ws = new_workspace(ckv_q8_workspace_size(cache, self.graph, self.sel), device=dev)
+
+    def grow(self, add: torch.Tensor, rows: int, stream=None) -> Plan:
+        """Request b changes by add[b] tokens (int32 [B] on the device); rows
+        bounds the tokens that this call may add."""
+        plan = self._plans.get(rows)
+        if plan is None:
+            plan = self._plans[rows] = new_plan(self.cache, rows)
+        with _range("ckv_plan_blocks"):
+            ckv_plan_blocks(self.cache, add, plan, stream)
+        self.plan = plan
+        return plan
+
+    def write(self, k_new: torch.Tensor, v_new: torch.Tensor, stream=None) -> None:
+        """The rows of the last grow(): packed [rows, Hkv, d] or padded [B, T, Hkv, d]."""
+        if self.plan is None:
+            raise RuntimeError("write() follows grow()")
+        with _range("ckv_quant_append"):
+            ckv_quant_append(self.cache, self.plan, k_new, v_new, stream)
+
+    def read(self, R: int, first: Optional[torch.Tensor] = None, stream=None):
+        """Positions first[b] .. first[b] + R - 1 of every request as [B, Hkv, R, d] pairs."""
+        c = self.cache
+        k = torch.empty((c.B, c.Hkv, R, c.d), dtype=c.dtype, device=c.device)
+        v = torch.empty_like(k)
+        with _range("ckv_q8_read"):
+            ckv_q8_read(c, k, v, first, stream)
+        return k, v
+
+    def dense(self, q: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        out = self.out if out is None else out
+        with _range("ckv_dense_decode_q8"):
+            ckv_dense_decode_q8(self.cache, q, out, self.ws, stream)
+        return out
+
+    def build(self, labels: torch.Tensor, T: int, stream=None) -> None:
+        """Community state from labels (int32 [U, >= T]) over positions [0, T),
+        which every request must hold; the centres are those of the values held."""
+        k, v = self.read(T, stream=stream)
+        s = self.shape
+        rows = CacheDesc(s.dtype, s.B, s.Hkv, s.Hq, s.d, s.T_cap, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
+                         k.stride(2))
+        with _range("ckv_build_centroids"):
+            ckv_build_centroids(rows, labels, T, self.graph, self.graph_ws, stream)
+
+    def select(self, q: torch.Tensor, budget: int, stream=None) -> None:
+        with _range("ckv_score_select"):
+            ckv_score_select(self.shape, self.graph, q, budget, self.sel, self.graph_ws, stream)
+
+    def attend(self, q: torch.Tensor, k_new: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Attention over the selection; with k_new the new tokens also join
+        communities (nbr8, assigned), each at its request's length."""
+        with _range("ckv_sparse_decode_q8"):
+            if k_new is None:
+                ckv_sparse_decode_q8(self.cache, q, self.graph, self.sel, self.out, None, self.ws, stream=stream)
+            else:
+                ckv_sparse_decode_q8(self.cache, q, self.graph, self.sel, self.out, self.nbr8, self.ws, k_new,
+                                     self.assigned, stream)
+        return self.out

@@ -771,3 +771,91 @@ def test_the_debug_build_gives_the_same():
     assert dbg.ckv_dense_decode_q8(ctypes.byref(cache.desc), q.data_ptr(), b.data_ptr(), ws.data_ptr(), ws.numel(), st) == 0
     torch.cuda.synchronize()
     assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------------------
+# a layer's decode, as it is used
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("mode", ["group", "head"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_paged_layer_decodes_with_communities(mode, fmt):
+    """Prompts written, communities built, then decode steps (select, attend with the join, grow, write) against the
+    references: selections and joins of the oracle on the values that the cache holds."""
+    from graph_community_sparse_b200.layer import PagedLayerState
+
+    B, Hkv, Hq, d, T, S, C, steps = 2, 2, 4, 64, 300, 4, 10, 4
+    gen = torch.Generator().manual_seed(17)
+    cache = ckv.new_q8_cache(B, Hkv, Hq, d, 60, 16, 25, fmt, torch.float32)
+    st = PagedLayerState(cache, mode, S, C, 8, T_cap=400)
+    G = Hkv if mode == "group" else Hq
+    mu = torch.randn((C, d), generator=gen)
+    lab = torch.randint(0, C, (B, Hkv, T), generator=gen)
+    K = (mu[lab] + 0.3 * torch.randn((B, Hkv, T, d), generator=gen)).to(DEV)
+    V = torch.randn((B, Hkv, T, d), generator=gen).to(DEV)
+    st.grow(i32([T, T]), B * T)
+    st.write(K.transpose(1, 2), V.transpose(1, 2))
+    labels = lab[:, :, None, :].expand(B, Hkv, G // Hkv, T).reshape(B * G, T).to(torch.int32).clone()
+    labels[:, :S] = -1
+    st.build(labels.to(DEV), T)
+    blocks, refs = table_lists(cache), refs_of(cache)
+    states = [O.GraphState(labels[u].numpy(), 400, S, C) for u in range(B * G)]
+    # the keys that the centres average: the values held when the graphs were built, then the new tokens' own rows
+    keys = np.zeros((B, Hkv, 400, d))
+    for b in range(B):
+        keys[b, :, :T] = refs[0].rows(blocks, b, range(T)).transpose(1, 0, 2)
+    one = i32([1] * B)
+    for step in range(steps):
+        q = (0.5 * mu[torch.randint(0, C, (B, Hq), generator=gen)] + torch.randn((B, Hq, d), generator=gen)).to(DEV)
+        kn, vn = torch.randn((2, B, Hkv, d), generator=gen).to(DEV)
+        kn = kn + mu[0].to(DEV)
+        st.select(q, 90)
+        out = st.attend(q, kn).clone()
+        lists = []
+        for u in range(B * G):
+            n = int(st.sel.n_tok[u])
+            lists.append(st.sel.sel_tok[u, :n].tolist())
+            b, g = divmod(u, G)
+            kv = g if mode == "group" else g * Hkv // Hq
+            heads = range(g * Hq // Hkv, (g + 1) * Hq // Hkv) if mode == "group" else [g]
+            n_tok = blocks.len[b]
+            members = states[u].members()
+            cent, cnt = O.centroids(keys[b, kv], members)
+            scores = O.community_scores(q[b, list(heads)].double().cpu().numpy(), cent, cnt)
+            got = st.sel.sel_comm[u, : int(st.sel.n_sel[u])].tolist()
+            want = O.select(scores, cnt, 90)
+            # scores are fp32 sums of 64 products, a few units in size: 64 * 2^-24 * 8 < 1e-4
+            cut = scores[want[-1]]
+            assert all(abs(scores[c] - cut) < 1e-4 for c in set(got) ^ set(want)), (got, want)
+            assert sorted(lists[-1]) == sorted(O.token_set(got, members, S).tolist())
+            # the join: a candidate of the best score
+            asg = int(st.assigned[u])
+            cands = [int(states[u].comm_of[p]) for p in st.nbr8[u].tolist() if p >= 0]
+            kk = kn[b, kv].double().cpu().numpy()
+            best = max(float(kk @ cent[c]) for c in cands)
+            assert asg in cands and best - float(kk @ cent[asg]) < 1e-4 * max(1.0, abs(best))
+            states[u].comm_of[n_tok] = asg
+            states[u].T = n_tok + 1
+        check_out(cache, q, out, lists, mode == "group")
+        p = st.grow(one, B)
+        st.write(kn, vn)
+        _, _, granted, _ = blocks.change([1] * B, B)
+        for ref, x in zip(refs, (kn, vn)):
+            ref.append(blocks, granted, split_rows(x.cpu(), [1] * B))
+        check_table(cache, blocks)
+        keys[:, :, T + step] = kn.double().cpu().numpy()
+        assert p.granted.tolist() == [1] * B
+    check_pool(cache, refs, blocks)
+    check_out(cache, q, st.dense(q))
+    assert cache.len.tolist() == [T + steps] * B
+    assert ckv.ckv_get_device_error(cache) == 0 and int(st.graph.dev_err) == 0
+
+
+def test_paged_layer_write_follows_grow():
+    from graph_community_sparse_b200.layer import PagedLayerState
+
+    st = PagedLayerState(ckv.new_q8_cache(1, 1, 1, 64, 4, 16, 4))
+    with pytest.raises(RuntimeError):
+        st.write(torch.zeros((1, 1, 64), dtype=torch.bfloat16, device=DEV), torch.zeros((1, 1, 64), dtype=torch.bfloat16, device=DEV))
+    k, v = st.read(5)
+    assert k.shape == (1, 1, 5, 64) and (k == 0).all() and (v == 0).all()
