@@ -66,30 +66,32 @@ struct BlocksQ8Smem {
     static constexpr int WARP = QdShape<D, LIST>::STAGES * Q8Geom<D, QdShape<D, LIST>::NH>::SLOT;  // a warp's ring, then its accumulators
     static constexpr int FIXED = QD_WARPS * WARP + 2 * QD_WARPS * GQ * 4;
     static_assert(GQ * D * 4 <= WARP, "a warp's accumulators fit its ring");
-    // the join of a unit's partials: weights and sums of JOIN slots at a time
-    static constexpr int JOIN = 128;
-    static_assert(2 * JOIN * GQ * 4 + QD_THREADS * 16 <= QD_WARPS * WARP, "the join fits the rings");
+    // the join of a unit's partials: JOIN rows at a time, with their references and sums
+    static constexpr int FIT = (QD_WARPS * WARP - QD_THREADS * 16) / (GQ * D * 4 + 2 * GQ * 4);
+    static constexpr int JOIN = FIT < 64 ? FIT / 4 * 4 : 64;
+    static_assert(JOIN >= 8, "the join fits the rings");
 };
 
-// Joins the partials of a unit that blocks c0 .. c0 + np - 1 share into out, JOIN
-// at a time.  A block's first segment has its even slot, its last (when that is
-// another) the odd one: `odd` for block c0.  References
-// and sums first, all at once, then the weighted rows with the slots shared out
-// over the threads.
+// Joins the partials of a unit that blocks c0 .. c0 + np - 1 share into out.  A
+// block's first segment has its even slot, its last (when that is another) the odd
+// one: `odd` for block c0.  A chunk of rows at a time comes into the rings' memory
+// by asynchronous copies, all in flight at once, with the references and sums
+// (loads into registers, 16 at a time, took 2 us longer for 55 rows).
 template <int D, int GQ, bool LIST>
 __device__ __forceinline__ void join_partials(const BlocksQ8Params& p, int c0, int np, int odd, float* out,
                                               unsigned char* smem, float* s_head, int tid) {
-    constexpr int JOIN = BlocksQ8Smem<D, GQ, LIST>::JOIN;
+    using SM = BlocksQ8Smem<D, GQ, LIST>;
     constexpr int VECS = GQ * D / 4;  // float4 of an output
     constexpr int SHARE = QD_THREADS / VECS > 0 ? QD_THREADS / VECS : 1;      // threads to a float4
     constexpr int PER = SHARE > 1 ? 1 : (VECS + QD_THREADS - 1) / QD_THREADS;  // float4 to a thread
     const int lane = tid & 31, warp = tid >> 5;
     float* s_f = reinterpret_cast<float*>(smem);  // [JOIN][GQ] references, then weights
-    float* s_l = s_f + JOIN * GQ;                 // [JOIN][GQ] sums
-    float4* s_part = reinterpret_cast<float4*>(s_l + JOIN * GQ);
-    float* s_m = s_head;                          // [GQ] running reference, sum and the old rows' factor
+    float* s_l = s_f + SM::JOIN * GQ;             // [JOIN][GQ] sums
+    float4* s_part = reinterpret_cast<float4*>(s_l + SM::JOIN * GQ);
+    float4* s_rows = s_part + QD_THREADS;         // [JOIN][VECS]
+    float* s_m = s_head;                          // [GQ] running reference, then sum
     float* s_sum = s_head + GQ;
-    __shared__ float s_old[GQ];
+    __shared__ float s_old[GQ];                   // the old rows' factor
     if (tid < GQ) {
         s_m[tid] = Q8_M_INIT;
         s_sum[tid] = 0.f;
@@ -98,10 +100,14 @@ __device__ __forceinline__ void join_partials(const BlocksQ8Params& p, int c0, i
     float4 A[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) A[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < np; i0 += JOIN) {
-        const int n = min(np - i0, JOIN);
-        __syncthreads();
+    for (int i0 = 0; i0 < np; i0 += SM::JOIN) {
+        const int n = min(np - i0, SM::JOIN);
         auto slot_of = [&](int i) { return 2 * (c0 + i0 + i) + (i0 + i == 0 ? odd : 0); };
+        __syncthreads();
+        const float4* acc = reinterpret_cast<const float4*>(p.acc);
+        for (int x = tid; x < n * VECS; x += QD_THREADS)
+            cp_async_16i<0, 0>(smem_addr32(s_rows + x), acc + (size_t)slot_of(x / VECS) * VECS + x % VECS);
+        cp_async_commit();
         for (int x = tid; x < n * GQ; x += QD_THREADS) {
             const int at = slot_of(x / GQ) * GQ + x % GQ;
             s_f[x] = __ldcg(p.m + at);
@@ -128,20 +134,20 @@ __device__ __forceinline__ void join_partials(const BlocksQ8Params& p, int c0, i
                 s_sum[h] = fmaf(s_sum[h], f, L);
             }
         }
+        cp_async_wait<0>();
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
             const int x = x0 + k * QD_THREADS, h = x / (D / 4);
             if (x >= VECS || part >= SHARE) continue;
-            const float4* acc = reinterpret_cast<const float4*>(p.acc) + x;
             const float fo = s_old[h];
             A[k].x *= fo;
             A[k].y *= fo;
             A[k].z *= fo;
             A[k].w *= fo;
-#pragma unroll 16
+#pragma unroll 4
             for (int i = part; i < n; i += SHARE) {
-                const float4 v = __ldcg(acc + (size_t)slot_of(i) * VECS);
+                const float4 v = s_rows[i * VECS + x];
                 const float f = s_f[i * GQ + h];
                 A[k].x = fmaf(v.x, f, A[k].x);
                 A[k].y = fmaf(v.y, f, A[k].y);
@@ -206,7 +212,7 @@ __global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_
     using SM = BlocksQ8Smem<D, GQ, LIST>;
     constexpr int STAGES = SH::STAGES, TOK = SH::TOK;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ int s_last;
+    __shared__ int s_last, s_red[2][QD_WARPS], s_at[2];
     const TableView& t = p.c.t;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // groups of units of one length: requests with Hkv units each, or single lists
@@ -215,10 +221,13 @@ __global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_
     unsigned char* ring = smem + warp * SM::WARP;
     float* wm = reinterpret_cast<float*>(smem + QD_WARPS * SM::WARP);  // [warps][GQ]
     float* wl = wm + QD_WARPS * GQ;
-    int* s_nt = reinterpret_cast<int*>(smem + SM::FIXED);              // [B] tiles of a unit of group b
+    int* s_n = reinterpret_cast<int*>(smem + SM::FIXED);               // [B] tokens of a unit of group b
     pdl_wait();
 
-    for (int b = tid; b < B; b += QD_THREADS) {
+    // thread i has the groups [b0, b1)
+    const int seg = (B + QD_THREADS - 1) / QD_THREADS;
+    const int b0 = min(B, tid * seg), b1 = min(B, b0 + seg);
+    for (int b = b0; b < b1; ++b) {
         int n;
         if constexpr (LIST) {
             n = max(0, min(p.n_tok[b], p.tok_cap));
@@ -229,16 +238,25 @@ __global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_
                 n = 0;
             }
         }
-        s_nt[b] = (n + TOK - 1) / TOK;
+        s_n[b] = n;
     }
-    __syncthreads();
-    // from here every warp works for itself, 32 groups at a time
+    auto tiles_of = [&](int b) { return (int)(((unsigned)s_n[b] + TOK - 1) / TOK); };
     auto ceil_div = [](int a, int b) { return (int)(((unsigned)a + b - 1) / (unsigned)b); };
     auto pieces = [&](int nt, int piece) { return nt <= QD_WHOLE ? min(nt, 1) : ceil_div(nt, piece); };
+    // the block's sum of f over the groups' tiles; one barrier (two buffers: a thread
+    // that runs ahead to the next sum does not touch what others still read)
+    int turn = 0;
     auto sum_over = [&](auto f) {
         int own = 0;
-        for (int b = lane; b < B; b += 32) own += f(s_nt[b]);
-        return __reduce_add_sync(FULL, own);
+        for (int b = b0; b < b1; ++b) own += f(tiles_of(b));
+        own = __reduce_add_sync(FULL, own);
+        if (lane == 0) s_red[turn][warp] = own;
+        __syncthreads();
+        int all = 0;
+#pragma unroll
+        for (int w = 0; w < QD_WARPS; ++w) all += s_red[turn][w];
+        turn ^= 1;
+        return all;
     };
     const int total = sum_over([](int nt) { return nt; }) * H;
     if (total == 0) {
@@ -274,34 +292,44 @@ __global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_
         }
     };
     for (int b = blockIdx.x; b < B; b += grid)
-        if (s_nt[b] == 0) {  // nothing to attend to
+        if (s_n[b] == 0) {  // nothing to attend to
             int kvh;
             float* o = p.out + first_row(b, 0, kvh) * D;
             for (int i = tid; i < H * GQ * D; i += QD_THREADS) o[i] = 0.f;
         }
 
+    if (start >= end) return;
+    // the group of `start`, and what comes before it: the thread whose groups hold it finds it
+    {
+        auto weight = [&](int b) { return (piece ? pieces(tiles_of(b), piece) : tiles_of(b)) * H; };
+        int own = 0;
+        for (int b = b0; b < b1; ++b) own += weight(b);
+        int inc = own;
+#pragma unroll
+        for (int y = 1; y < 32; y <<= 1) {
+            const int z = __shfl_up_sync(FULL, inc, y);
+            if (lane >= y) inc += z;
+        }
+        if (lane == 31) s_red[turn][warp] = inc;
+        __syncthreads();
+        int pre = inc - own;
+#pragma unroll
+        for (int w = 0; w < QD_WARPS; ++w) pre += w < warp ? s_red[turn][w] : 0;
+        if (pre <= start && start < pre + own) {
+            int b = b0;
+            while (start >= pre + weight(b)) pre += weight(b++);
+            s_at[0] = b;
+            s_at[1] = pre;
+        }
+        __syncthreads();
+    }
+    int b = s_at[0], pre = s_at[1];  // the group, and what comes before it
+
     W st;
     for (int at = start; at < end;) {
         // the segment: tiles [lo, hi) of unit h of group b, the unit shared by the blocks c0 .. c0 + np - 1
-        int b = 0, pre = 0;  // pre: what comes before group b
-        for (int k = 0;; k += 32) {
-            const int x = k + lane < B ? s_nt[k + lane] : 0;
-            int own = (piece ? pieces(x, piece) : x) * H, inc = own;
-#pragma unroll
-            for (int y = 1; y < 32; y <<= 1) {
-                const int z = __shfl_up_sync(FULL, inc, y);
-                if (lane >= y) inc += z;
-            }
-            const int chunk = __shfl_sync(FULL, inc, 31);
-            if (at < pre + chunk) {  // the first group that ends past `at`
-                const int l = __ffs(__ballot_sync(FULL, at < pre + inc)) - 1;
-                b = k + l;
-                pre += __shfl_sync(FULL, inc - own, l);
-                break;
-            }
-            pre += chunk;
-        }
-        const int nt = s_nt[b];
+        while (at >= pre + tiles_of(b) * H && !piece) pre += tiles_of(b++) * H;
+        const int n = s_n[b], nt = tiles_of(b);
         int h, lo, hi, c0, np, odd = 0, slot = 2 * blockIdx.x;
         if (piece) {
             np = pieces(nt, piece);
@@ -327,8 +355,6 @@ __global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_
         const auto raw_q = W::fetch_q(W::q_row(p.q, p.c.dtype, row0), p.c.dtype, lane);
         const int seq = LIST ? b / p.G : b;
         const int32_t* table = t.table + (size_t)seq * t.max_blocks;
-        // n: the unit's tokens (list entries)
-        const int n = LIST ? max(0, min(p.n_tok[b], p.tok_cap)) : t.len[b];
 
         const int nit = (hi - lo - warp + QD_WARPS - 1) / QD_WARPS;  // this warp's tiles: lo + warp + QD_WARPS i
         const unsigned ring32 = smem_addr32(ring);
