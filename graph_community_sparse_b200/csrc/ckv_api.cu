@@ -170,8 +170,8 @@ ckv_status check_table(const ckv_table_desc* t, bool pool) {
     if (t->block != 16 && t->block != 32 && t->block != 64 && t->block != 128)
         return fail(CKV_ERR_UNSUPPORTED, "block = %d not in {16,32,64,128}", t->block);
     if (t->B > ckv::MAX_UNITS) return fail(CKV_ERR_UNSUPPORTED, "B = %d above %d", t->B, ckv::MAX_UNITS);
-    if ((int64_t)t->n_blocks * t->block > 0x7fffffffll || (int64_t)t->max_blocks * t->block > 0x7fffffffll)
-        return fail(CKV_ERR_UNSUPPORTED, "n_blocks * block or max_blocks * block above 2^31 - 1");
+    if ((int64_t)t->n_blocks * t->block > 0x7fffffffll || (int64_t)t->max_blocks * t->block > (int64_t)1 << 30)
+        return fail(CKV_ERR_UNSUPPORTED, "n_blocks * block above 2^31 - 1 or max_blocks * block above 2^30");
     if (!t->table || !t->len || !t->dev_err) return fail(CKV_ERR_INVALID_ARG, "table, len or dev_err is NULL");
     if (pool && (!t->free_list || !t->n_free)) return fail(CKV_ERR_INVALID_ARG, "free_list or n_free is NULL");
     return CKV_OK;
@@ -277,7 +277,7 @@ size_t q8_ws_bytes(const ckv_q8_desc* c, const ckv_graph_desc* g, int tok_cap) {
         const size_t s = ckv::decode_ws_bytes(c->blocks.B * G, c->Hq / G, c->d, tok_cap);
         need = need > s ? need : s;
     }
-    return ckv::WS_RESERVED + ckv::q8_counter_bytes(c->blocks.B * c->Hq) + need;
+    return ckv::WS_RESERVED + ckv::Q8_COUNTER_BYTES + need;
 }
 
 #define CKV_TRY(expr)                      \

@@ -204,7 +204,9 @@ __global__ void __launch_bounds__(D + (DENSE ? 0 : 32 * NBR_WARPS), 2) decode_me
         const int n = uend - ubeg;
         const float* lamu = ws.lam + (size_t)u * ws.lam_cap;
         const int32_t* toks = p.sel_tok + (size_t)u * p.tok_cap;
-        auto key_at = [&](int i) { return nbr_key(lamu[i], __ldg(toks + i)); };
+        // an 8-bit cache's skipped entry (logit -inf) is no neighbour
+        auto key_of = [&](float lam, int pos) { return Q8 && lam == -INFINITY ? 0ull : nbr_key(lam, pos); };
+        auto key_at = [&](int i) { return key_of(lamu[i], __ldg(toks + i)); };
         // all loads first (clamped in-range indices, no branches), so the
         // 2 x NBR_KEEP loads are in flight together
         float lv[NBR_KEEP];
@@ -218,7 +220,7 @@ __global__ void __launch_bounds__(D + (DENSE ? 0 : 32 * NBR_WARPS), 2) decode_me
         unsigned long long kk[NBR_KEEP];
 #pragma unroll
         for (int k = 0; k < NBR_KEEP; ++k)
-            kk[k] = p.S + xt + k * NBR_THREADS < n ? nbr_key(lv[k], pv[k]) : 0ull;
+            kk[k] = p.S + xt + k * NBR_THREADS < n ? key_of(lv[k], pv[k]) : 0ull;
         unsigned long long mx = 0;
 #pragma unroll
         for (int k = 0; k < NBR_KEEP; ++k) mx = kk[k] > mx ? kk[k] : mx;

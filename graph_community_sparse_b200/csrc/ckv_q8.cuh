@@ -44,9 +44,10 @@ struct RowsView {  // new rows in, or read-back rows out
 cudaError_t launch_plan_blocks(const TableView& t, const int32_t* add, const PlanView& p, cudaStream_t st);
 cudaError_t launch_quant_append(const Q8View& c, const PlanView& p, const RowsView& r, cudaStream_t st);
 cudaError_t launch_q8_read(const Q8View& c, const int32_t* first, int R, const RowsView& r, cudaStream_t st);
-// The attention's workspace: a counter per (request, query head) after the head,
-// then the larger of the two calls' partials.
-size_t q8_counter_bytes(int units);
+// The attention's workspace: counters of the units after the head (of the most there
+// can be, so that they are in the same place for every cache), then the larger of
+// the two calls' partials.
+constexpr size_t Q8_COUNTER_BYTES = (size_t)MAX_UNITS * 4;
 size_t q8_blocks_ws_bytes(int gq, int d);
 cudaError_t launch_dense_decode_q8(const Q8View& c, const void* q, float* out, void* ws, cudaStream_t st);
 cudaError_t launch_sparse_decode_q8(const Q8View& c, const GraphView& g, const SelView& s, const void* q, float* out,

@@ -399,9 +399,10 @@ struct Q8Warp {
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        s[j][r][e] = on(j, r) ? s[j][r][e] : -INFINITY;
-                        // scales that were not copied are zero
-                        kf[j][r % NS][e] = kf[j][r % NS][e] == 0.f ? 1.f : kf[j][r % NS][e];
+                        // a scale of zero, or one that was not copied: the score is zero, and -inf stays -inf
+                        const bool none = kf[j][r % NS][e] == 0.f;
+                        s[j][r][e] = !on(j, r) ? -INFINITY : none ? 0.f : s[j][r][e];
+                        if (r == 1 || NS == 2) kf[j][r % NS][e] = none ? 1.f : kf[j][r % NS][e];
                     }
         }
 

@@ -566,10 +566,10 @@ static cudaError_t launch_blocks_q8_t(const BlocksQ8Params& p, long long tiles, 
 }
 
 // The workspace's parts after its head: the units' counters, then the partials.
-inline void carve_blocks_ws(BlocksQ8Params& p, void* ws, int gq, int counters) {
+inline void carve_blocks_ws(BlocksQ8Params& p, void* ws, int gq) {
     char* w = static_cast<char*>(ws) + WS_RESERVED;
     p.count = reinterpret_cast<int*>(w);
-    w += q8_counter_bytes(counters);
+    w += Q8_COUNTER_BYTES;
     p.m = reinterpret_cast<float*>(w);
     w += align256((size_t)2 * QD_MAX_GRID * gq * 4);
     p.l = reinterpret_cast<float*>(w);

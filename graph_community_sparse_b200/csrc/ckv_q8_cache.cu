@@ -375,9 +375,8 @@ __global__ void __launch_bounds__(APP_THREADS) append_kernel(const __grid_consta
         const int n = t.len[b], a = q.p.granted[b];
         int x = 0;
         if (a > 0) {
-            const bool ok = n >= a && (long long)n <= (long long)t.max_blocks * BS &&
-                            (q.r.T_rows ? a <= q.r.T_rows
-                                        : q.p.start[b] >= 0 && (long long)q.p.start[b] + a <= q.p.n_rows);
+            const bool ok = n >= a && (long long)n <= (long long)t.max_blocks * BS && q.p.start[b] >= 0 &&
+                            (long long)q.p.start[b] + a <= q.p.n_rows && (q.r.T_rows == 0 || a <= q.r.T_rows);
             if (ok) x = (n - 1) / BS - (n - a) / BS + 1;
             else if (blockIdx.x == 0) atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
         }

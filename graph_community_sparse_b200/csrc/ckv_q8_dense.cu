@@ -5,7 +5,6 @@
 
 namespace ckv {
 
-size_t q8_counter_bytes(int units) { return align256((size_t)units * 4); }
 size_t q8_blocks_ws_bytes(int gq, int d) {
     return align256((size_t)2 * QD_MAX_GRID * gq * 4) * 2 + align256((size_t)2 * QD_MAX_GRID * gq * d * 4);
 }
@@ -17,7 +16,7 @@ cudaError_t launch_dense_decode_q8(const Q8View& c, const void* q, float* out, v
     p.out = out;
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)c.d);
     const int gq = c.Hq / c.Hkv;
-    carve_blocks_ws(p, ws, gq, c.t.B * c.Hq);
+    carve_blocks_ws(p, ws, gq);
     const long long units = (long long)c.t.B * c.Hkv;
     const long long tiles = units * ((long long)c.t.max_blocks * c.t.block / (QD_MIN_PIECE * 32) + 1);
 #define CKV_QD(DD, GG)                                                                \

@@ -229,7 +229,7 @@ cudaError_t launch_sparse_decode_q8(const Q8View& c, const GraphView& g, const S
     d.unit_prefix = s.unit_prefix;
     d.n_tok = s.n_tok;
     d.scale_log2 = 1.4426950408889634f / sqrtf((float)c.d);
-    d.ws = carve_decode_ws(ws, WS_RESERVED + q8_counter_bytes(c.t.B * c.Hq), d.U, g.gq, c.d, s.tok_cap);
+    d.ws = carve_decode_ws(ws, WS_RESERVED + Q8_COUNTER_BYTES, d.U, g.gq, c.d, s.tok_cap);
     d.want_nbr = nbr8 != nullptr || k_new != nullptr;
     d.out = out;
     d.nbr8 = nbr8;
@@ -260,7 +260,7 @@ cudaError_t launch_sparse_decode_q8(const Q8View& c, const GraphView& g, const S
         b.tok_cap = d.tok_cap;
         b.sel_tok = d.sel_tok;
         b.n_tok = d.n_tok;
-        carve_blocks_ws(b, ws, g.gq, c.t.B * c.Hq);
+        carve_blocks_ws(b, ws, g.gq);
         const long long tiles = (long long)d.U * (d.tok_cap / (QD_MIN_PIECE * 16) + 1);
 #define CKV_QL(DD, GG)                                                                  \
         if (c.d == DD && g.gq == GG)                                                    \

@@ -401,8 +401,8 @@ CKV_API ckv_status ckv_build_edges(const ckv_cache_desc* cache, int32_t mode, in
  * Every length, slot and block id that a kernel uses is checked on the device
  * in every build: a bad one sets CKV_DEVERR_BLOCK and the tokens that it names
  * are skipped (attention, append) or read as zeros (ckv_q8_read).
- * block is 16, 32, 64 or 128; max_blocks >= 1; 1 <= B <= 8192;
- * n_blocks * Hkv * block < 2^31.
+ * block is 16, 32, 64 or 128; max_blocks >= 1; max_blocks * block <= 2^30;
+ * 1 <= B <= 8192; B * Hkv <= 8192; n_blocks * Hkv * block < 2^31.
  */
 typedef enum { CKV_Q8_INT8 = 0, CKV_Q8_E4M3 = 1 } ckv_q8_format;
 
@@ -420,7 +420,7 @@ typedef struct {
 
 /*
  * k, v: codes [n_blocks, Hkv, block, d], contiguous, 16-byte aligned.
- * k_scale, v_scale: fp32 [n_blocks, Hkv].  dtype: that of q and of the rows
+ * k_scale, v_scale: fp32 [n_blocks, Hkv], not negative.  dtype: that of q and of the rows
  * appended and read back.
  */
 typedef struct {
@@ -515,11 +515,11 @@ CKV_API ckv_status ckv_q8_read(const ckv_q8_desc* cache, const int32_t* first, i
 
 /*
  * Workspace of the two attention calls below (graph and sel NULL: the dense
- * one alone).  Unlike the other calls' it keeps a counter per (request, query head):
+ * one alone).  Unlike the other calls' it keeps counters beyond its head:
  * zero-fill the whole workspace once after allocating it, and give it to these
- * two calls only, with the B and Hq that it was sized for; every call leaves the
- * counters zero.  Calls sharing it must not overlap on the GPU (graphs captured
- * with one workspace included).
+ * two calls only (of any 8-bit cache that it is large enough for); every call
+ * leaves the counters zero.  Calls sharing it must not overlap on the GPU (graphs
+ * captured with one workspace included).
  */
 CKV_API ckv_status ckv_q8_workspace_size(const ckv_q8_desc* cache, const ckv_graph_desc* graph,
                                          const ckv_selection_desc* sel, size_t* bytes);
@@ -528,7 +528,8 @@ CKV_API ckv_status ckv_q8_workspace_size(const ckv_q8_desc* cache, const ckv_gra
  * ckv_dense_decode over the 8-bit cache: exact softmax attention of one token's
  * queries q [B, Hq, d] (cache dtype, contiguous) over positions [0, len[b]) of
  * each request; out fp32 [B, Hq, d], zeros where len[b] = 0.  Codes are exact
- * in the products, the softmax's statistics and sums are fp32.  One launch.
+ * in the products, the softmax's statistics and sums are fp32; magnitudes of q
+ * below 2^90.  One launch.
  */
 CKV_API ckv_status ckv_dense_decode_q8(const ckv_q8_desc* cache, const void* q, float* out, void* ws, size_t ws_bytes,
                                        ckv_stream_t stream);
@@ -537,7 +538,8 @@ CKV_API ckv_status ckv_dense_decode_q8(const ckv_q8_desc* cache, const void* q, 
  * ckv_sparse_decode over the 8-bit cache: the selected positions of sel (from
  * ckv_score_select, whose cache descriptor then needs shapes only: k = v =
  * NULL, the graph's T_cap) are read through the block table.  out, nbr8 as
- * there; entries outside [0, len[b]) or in a bad block are skipped.
+ * there; entries outside [0, len[b]) or in a bad block are skipped (and are no
+ * neighbours).
  * k_new [B, Hkv, d] (cache dtype, contiguous) not NULL: the new token, which
  * will be position len[b] of request b, also joins a community of every
  * graph unit as in ckv_sparse_decode_append (same rule and results; assigned

@@ -340,6 +340,9 @@ def test_append_bad_plans_are_flagged_and_skipped():
     go([0, 5], [0, 1, 2, 3, 4], [5])                  # a length past the table
     cache.len.fill_(5)
     go([0, 5], [0, 1, 2, 3, 4], [5], torch.ones((1, 3, 1, 64), dtype=torch.bfloat16, device=DEV))  # past the padding
+    padded = torch.ones((1, 5, 1, 64), dtype=torch.bfloat16, device=DEV)
+    go([3, 8], [0, 1, 2, 3, 4], [5], padded)          # slots past the slot map, whatever the rows' layout
+    go([-1, 4], [0, 1, 2, 3, 4], [5], padded)
 
 
 def test_read_bad_blocks_are_zeros():
@@ -474,6 +477,31 @@ def test_dense_scales_of_very_different_size(fmt, gq):
     check_out(cache, q, out)
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("gq", [4, 8])
+def test_scales_of_zero(fmt, gq):
+    """Blocks of all zeros kept with a scale of zero: scores and values of zero, in whole tiles, part-filled ones and
+    lists."""
+    lens = [100, 5, 32, 77]
+    cache = filled(lens, 1, gq, 64, 16, fmt, torch.float32, seed=12)
+    for b, blocks in enumerate(([0, 3], [0], [0, 1], [4])):
+        for j in blocks:
+            x = int(cache.table[b, j])
+            cache.k_scale[x] = 0.0
+            if b != 2 or j:
+                cache.v_scale[x] = 0.0
+    q = torch.randn((4, gq, 64), device=DEV)
+    out = torch.full(q.shape, float("nan"), device=DEV)
+    ckv.ckv_dense_decode_q8(cache, q, out, workspace(cache))
+    check_out(cache, q, out)
+    lists = [list(range(0, n, 2)) for n in lens]
+    graph, sel = sparse_state(cache, lists, True, 0, 112)
+    for nbr in (None, torch.empty((4, 8), dtype=torch.int32, device=DEV)):
+        out.fill_(float("nan"))
+        ckv.ckv_sparse_decode_q8(cache, q, graph, sel, out, nbr, workspace(cache, graph, sel))
+        check_out(cache, q, out, lists)
+
+
 def test_dense_one_token_far_in_a_large_pool():
     """Rows beyond 2^32 bytes of the pool."""
     Hkv, block, d = 8, 128, 128
@@ -594,10 +622,39 @@ def test_sparse_lists(fmt, dtype, d, gq, group):
             assert nbr[u].tolist() == [-1] * 8
         else:
             check_neighbours(nbr[u].tolist(), qn, K, np.asarray(pos), 3, band=2 * 14 * 2.0 ** -23 * S)
-    # without neighbours: the same outputs
-    out2 = torch.full_like(out, float("nan"))
-    ckv.ckv_sparse_decode_q8(cache, q, graph, sel, out2, None, ws)
-    assert torch.allclose(out, out2, rtol=0, atol=1e-5)
+    # without neighbours, by the other kernel
+    out.fill_(float("nan"))
+    ckv.ckv_sparse_decode_q8(cache, q, graph, sel, out, None, ws)
+    check_out(cache, q, out, lists, group)
+    first = out.clone()
+    ckv.ckv_sparse_decode_q8(cache, q, graph, sel, out, None, ws)
+    assert torch.equal(first, out) and not ws[: 256 + 32768].any()
+
+
+@pytest.mark.parametrize("group", [True, False])
+@pytest.mark.parametrize("B,n", [(40, 90), (3, 2500), (130, 20)])
+def test_sparse_many_lists_and_long_ones(group, B, n):
+    """More lists than blocks, lists that many blocks share, and a workspace that two caches use in turn."""
+    Hkv, gq, d = 2, 4, 64
+    lens = [n + (b * 7) % 31 for b in range(B)]
+    cache = filled(lens, Hkv, Hkv * gq, d, 32, "int8", torch.bfloat16, seed=B)
+    G = Hkv if group else Hkv * gq
+    lists = random_lists(lens, G, [n, n // 2, 1, n - 3, 0, 16], 0, random.Random(B))
+    graph, sel = sparse_state(cache, lists, group, 0, cache.desc.blocks.max_blocks * 32)
+    q = torch.randn((B, Hkv * gq, d), device=DEV).bfloat16()
+    ws = workspace(cache, graph, sel)
+    other = filled([70, 900], 1, 8, 128, 16, "e4m3", torch.bfloat16, seed=1)
+    q2 = torch.randn((2, 8, 128), device=DEV).bfloat16()
+    out2 = torch.empty(q2.shape, device=DEV)
+    if ws.numel() < ckv.ckv_q8_workspace_size(other):
+        ws = workspace(other)
+    for _ in range(2):
+        out = torch.full(q.shape, float("nan"), device=DEV)
+        ckv.ckv_sparse_decode_q8(cache, q, graph, sel, out, None, ws)
+        ckv.ckv_dense_decode_q8(other, q2, out2, ws)
+        ckv.ckv_dense_decode_q8(cache, q, torch.empty_like(out), ws)
+    check_out(cache, q, out, lists, group)
+    check_out(other, q2, out2)
 
 
 def test_sparse_all_tokens_equals_dense():
@@ -632,6 +689,12 @@ def test_sparse_bad_entries_are_skipped():
     assert ckv.ckv_get_device_error(cache, reset=True) == ckv.DEVERR_BLOCK
     check_out(cache, q, out, [good, []])
     assert set(nbr[0].tolist()) <= set(good)
+    assert nbr[1].tolist() == [-1] * 8  # a skipped entry is no neighbour
+    # the same without neighbours (one launch)
+    out.fill_(float("nan"))
+    ckv.ckv_sparse_decode_q8(cache, q, graph, sel, out, None, ws)
+    assert ckv.ckv_get_device_error(cache, reset=True) == ckv.DEVERR_BLOCK
+    check_out(cache, q, out, [good, []])
 
 
 def test_sparse_joins_communities_like_the_wide_cache():
