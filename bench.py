@@ -97,13 +97,15 @@ def measured_peaks():
 def csrc_digest() -> str:
     """sha256 over the decode kernels' sources (every .cu and .cuh file but
     the host-only ckv_api.cu (argument checks) and ckv_timing.cu (diagnostic
-    events), and ckv_edges.cu, the prefill token graph's own translation unit,
-    which no decode kernel includes; names and contents, in name order): any
-    decode kernel or launch change alters it."""
+    events), and ckv_edges.cu and ckv_q8*, the translation units of the prefill
+    token graph and of the 8-bit cache, which no kernel of the step includes;
+    names and contents, in name order): any decode kernel or launch change
+    alters it."""
     d = os.path.join(ROOT, "graph_community_sparse_b200", "csrc")
     h = hashlib.sha256()
     for f in sorted(os.listdir(d)):
-        if f.endswith((".cu", ".cuh", ".h")) and f not in ("ckv_api.cu", "ckv_timing.cu", "ckv_edges.cu"):
+        if f.endswith((".cu", ".cuh", ".h")) and not f.startswith("ckv_q8") and f not in (
+                "ckv_api.cu", "ckv_timing.cu", "ckv_edges.cu"):
             h.update(f.encode() + b"\0" + open(os.path.join(d, f), "rb").read())
     return h.hexdigest()
 

@@ -269,13 +269,12 @@ ckv_status check_q8_graph(const ckv_q8_desc* c, const ckv_graph_desc* g) {
     return check_graph(&s, g);
 }
 
-// head, counters, then the larger of the two calls' parts
+// head, counters, partials (of the most heads a unit can have), then the lists' graph logits
 size_t q8_ws_bytes(const ckv_q8_desc* c, const ckv_graph_desc* g, int tok_cap) {
     size_t need = ckv::q8_blocks_ws_bytes(c->Hq / c->Hkv, c->d);
     if (g) {
-        const int G = g->mode == CKV_GRAPH_PER_HEAD ? c->Hq : c->Hkv;
-        const size_t s = ckv::decode_ws_bytes(c->blocks.B * G, c->Hq / G, c->d, tok_cap);
-        need = need > s ? need : s;
+        const int64_t U = (int64_t)c->blocks.B * (g->mode == CKV_GRAPH_PER_HEAD ? c->Hq : c->Hkv);
+        need += ckv::align256((size_t)U * tok_cap * 4);
     }
     return ckv::WS_RESERVED + ckv::Q8_COUNTER_BYTES + need;
 }

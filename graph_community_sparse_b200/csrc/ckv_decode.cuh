@@ -1,8 +1,8 @@
 // What the decode attention kernels share: the parameter pack, the work split
 // and the merge kernel that follows them (the units' partials combined, the
 // neighbour search over the stored graph logits, the fused community update).
-// Used by the attention over the 16/32-bit cache (ckv_decode.cu) and by the one
-// over an 8-bit cache's selected tokens (ckv_q8_sparse.cu).
+// The attention over the 16/32-bit cache (ckv_decode.cu) uses all of it, the one
+// over an 8-bit cache's selected tokens (ckv_q8_sparse.cu) the neighbour search.
 #pragma once
 
 #include <math.h>
@@ -136,12 +136,114 @@ __device__ __forceinline__ void merge_assign(const DecodeParams& p, int u, const
     }
 }
 
+// The neighbours of unit u, a list of n >= 1 entries, and its fused update, by
+// NBR_THREADS threads (xt of them).
+template <typename T, int D, bool Q8 = false>
+__device__ __forceinline__ void search_neighbours(const DecodeParams& p, int u, int n, int xt) {
+    // neighbour search over the graph logits the attention kernel stored,
+    // for the unit's non-sink list entries [S, n).  Threshold filter:
+    // theta = the 8th largest of the NBR_THREADS per-thread maxima is a
+    // distinct entry's key with 7 larger ones, so every top-8 entry has
+    // key >= theta; those few candidates are collected in shared memory
+    // and sorted by one warp.
+    __shared__ unsigned long long s_top[NBR_THREADS / 4];
+    __shared__ unsigned long long s_cand[NBR_CAP];
+    __shared__ int s_cnt;
+    const int lane = xt & 31, xw = xt >> 5;
+    const float* lamu = p.ws.lam + (size_t)u * p.ws.lam_cap;
+    const int32_t* toks = p.sel_tok + (size_t)u * p.tok_cap;
+    // an 8-bit cache's skipped entry (logit -inf) is no neighbour
+    auto key_of = [&](float lam, int pos) { return Q8 && lam == -INFINITY ? 0ull : nbr_key(lam, pos); };
+    auto key_at = [&](int i) { return key_of(lamu[i], __ldg(toks + i)); };
+    // all loads first (clamped in-range indices, no branches), so the
+    // 2 x NBR_KEEP loads are in flight together
+    float lv[NBR_KEEP];
+    int pv[NBR_KEEP];
+#pragma unroll
+    for (int k = 0; k < NBR_KEEP; ++k) {
+        const int i = min(p.S + xt + k * NBR_THREADS, n - 1);
+        lv[k] = lamu[i];
+        pv[k] = __ldg(toks + i);
+    }
+    unsigned long long kk[NBR_KEEP];
+#pragma unroll
+    for (int k = 0; k < NBR_KEEP; ++k)
+        kk[k] = p.S + xt + k * NBR_THREADS < n ? key_of(lv[k], pv[k]) : 0ull;
+    unsigned long long mx = 0;
+#pragma unroll
+    for (int k = 0; k < NBR_KEEP; ++k) mx = kk[k] > mx ? kk[k] : mx;
+    for (int i = p.S + xt + NBR_KEEP * NBR_THREADS; i < n; i += NBR_THREADS) {
+        const unsigned long long k2 = key_at(i);
+        mx = k2 > mx ? k2 : mx;
+    }
+    if (xt == 0) s_cnt = 0;
+    const unsigned long long srt = warp_sort_desc(mx, lane);
+    if (lane < 8) s_top[xw * 8 + lane] = srt;
+    asm volatile("bar.sync 1, %0;" ::"n"(NBR_THREADS) : "memory");
+    // every warp sorts the NBR_WARPS x 8 warp leaders itself (no extra barrier)
+    const unsigned long long theta =
+        __shfl_sync(FULL, warp_sort_desc(lane < NBR_WARPS * 8 ? s_top[lane] : 0ull, lane), 7);
+    auto offer = [&](unsigned long long k2) {
+        if (k2 != 0ull && k2 >= theta) {
+            const int slot = atomicAdd(&s_cnt, 1);
+            if (slot < NBR_CAP) s_cand[slot] = k2;
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < NBR_KEEP; ++k) offer(kk[k]);
+    for (int i = p.S + xt + NBR_KEEP * NBR_THREADS; i < n; i += NBR_THREADS) offer(key_at(i));
+    asm volatile("bar.sync 1, %0;" ::"n"(NBR_THREADS) : "memory");
+    __shared__ int s_nbpos[CKV_NEIGHBOURS];
+    if (xw == 0) {
+        const int cnt = s_cnt;
+        int32_t* outn = p.nbr8 ? p.nbr8 + (size_t)u * 8 : nullptr;
+        if (cnt <= 32) {
+            const unsigned long long x = warp_sort_desc(lane < cnt ? s_cand[lane] : 0ull, lane);
+            if (lane < 8) {
+                const int np = x ? nbr_pos(x) : -1;
+                s_nbpos[lane] = np;
+                if (outn) outn[lane] = np;
+            }
+        } else {
+            // many candidates (ties in the logits): 8 rounds, each taking
+            // the best key below the previous winner, from the shared
+            // list or, past its capacity, from the whole list
+            unsigned long long prev = ~0ull;
+            for (int r = 0; r < 8; ++r) {
+                unsigned long long best = 0;
+                if (cnt <= NBR_CAP) {
+                    for (int c = lane; c < cnt; c += 32) {
+                        const unsigned long long k2 = s_cand[c];
+                        if (k2 < prev && k2 > best) best = k2;
+                    }
+                } else {
+                    for (int i = p.S + lane; i < n; i += 32) {
+                        const unsigned long long k2 = key_at(i);
+                        if (k2 < prev && k2 > best) best = k2;
+                    }
+                }
+                best = warp_max_u64(best);
+                if (lane == 0) {
+                    const int np = best ? nbr_pos(best) : -1;
+                    s_nbpos[r] = np;
+                    if (outn) outn[r] = np;
+                }
+                prev = best;  // 0 once the entries run out: every later round finds none
+            }
+        }
+    }
+    if (p.append) {
+        asm volatile("bar.sync 1, %0;" ::"n"(NBR_THREADS) : "memory");  // s_nbpos complete
+        merge_assign<T, D, Q8>(p, u, s_nbpos, xt);
+    }
+}
+
 // One block per unit: threads 0..D-1 own one output dimension each (all the
 // unit's heads); the NBR_WARPS extra warps search the top-8 neighbours.  Slots are
 // combined in slot order, a chunk of slots at a time, by a per-thread online
 // merge: no shared memory and no barriers, so the merge costs about two
 // dependent rounds of loads.
-template <typename T, int D, int GQ, bool DENSE, bool Q8 = false>
+template <typename T, int D, int GQ, bool DENSE>
 __global__ void __launch_bounds__(D + (DENSE ? 0 : 32 * NBR_WARPS), 2) decode_merge(const __grid_constant__ DecodeParams p) {
     pdl_wait();  // the attention kernel's partials are complete and visible
     const int u = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -169,7 +271,7 @@ __global__ void __launch_bounds__(D + (DENSE ? 0 : 32 * NBR_WARPS), 2) decode_me
         if (!DENSE && p.append && warp >= D / 32) {
             __shared__ int s_none[CKV_NEIGHBOURS];
             if (t - D < CKV_NEIGHBOURS) s_none[t - D] = -1;
-            merge_assign<T, D, Q8>(p, u, s_none, t - D);  // no neighbour: the token joins nothing
+            merge_assign<T, D>(p, u, s_none, t - D);  // no neighbour: the token joins nothing
         }
         return;
     }
@@ -191,103 +293,7 @@ __global__ void __launch_bounds__(D + (DENSE ? 0 : 32 * NBR_WARPS), 2) decode_me
     const DecodeWs& ws = p.ws;
 
     if (!DENSE && p.want_nbr && warp >= D / 32) {
-        // neighbour search over the graph logits the attention kernel stored,
-        // for the unit's non-sink list entries [S, n).  Threshold filter:
-        // theta = the 8th largest of the NBR_THREADS per-thread maxima is a
-        // distinct entry's key with 7 larger ones, so every top-8 entry has
-        // key >= theta; those few candidates are collected in shared memory
-        // and sorted by one warp.
-        __shared__ unsigned long long s_top[NBR_THREADS / 4];
-        __shared__ unsigned long long s_cand[NBR_CAP];
-        __shared__ int s_cnt;
-        const int xt = t - D, xw = xt >> 5;
-        const int n = uend - ubeg;
-        const float* lamu = ws.lam + (size_t)u * ws.lam_cap;
-        const int32_t* toks = p.sel_tok + (size_t)u * p.tok_cap;
-        // an 8-bit cache's skipped entry (logit -inf) is no neighbour
-        auto key_of = [&](float lam, int pos) { return Q8 && lam == -INFINITY ? 0ull : nbr_key(lam, pos); };
-        auto key_at = [&](int i) { return key_of(lamu[i], __ldg(toks + i)); };
-        // all loads first (clamped in-range indices, no branches), so the
-        // 2 x NBR_KEEP loads are in flight together
-        float lv[NBR_KEEP];
-        int pv[NBR_KEEP];
-#pragma unroll
-        for (int k = 0; k < NBR_KEEP; ++k) {
-            const int i = min(p.S + xt + k * NBR_THREADS, n - 1);
-            lv[k] = lamu[i];
-            pv[k] = __ldg(toks + i);
-        }
-        unsigned long long kk[NBR_KEEP];
-#pragma unroll
-        for (int k = 0; k < NBR_KEEP; ++k)
-            kk[k] = p.S + xt + k * NBR_THREADS < n ? key_of(lv[k], pv[k]) : 0ull;
-        unsigned long long mx = 0;
-#pragma unroll
-        for (int k = 0; k < NBR_KEEP; ++k) mx = kk[k] > mx ? kk[k] : mx;
-        for (int i = p.S + xt + NBR_KEEP * NBR_THREADS; i < n; i += NBR_THREADS) {
-            const unsigned long long k2 = key_at(i);
-            mx = k2 > mx ? k2 : mx;
-        }
-        if (xt == 0) s_cnt = 0;
-        const unsigned long long srt = warp_sort_desc(mx, lane);
-        if (lane < 8) s_top[xw * 8 + lane] = srt;
-        asm volatile("bar.sync 1, %0;" ::"n"(NBR_THREADS) : "memory");
-        // every warp sorts the NBR_WARPS x 8 warp leaders itself (no extra barrier)
-        const unsigned long long theta =
-            __shfl_sync(FULL, warp_sort_desc(lane < NBR_WARPS * 8 ? s_top[lane] : 0ull, lane), 7);
-        auto offer = [&](unsigned long long k2) {
-            if (k2 != 0ull && k2 >= theta) {
-                const int slot = atomicAdd(&s_cnt, 1);
-                if (slot < NBR_CAP) s_cand[slot] = k2;
-            }
-        };
-#pragma unroll
-        for (int k = 0; k < NBR_KEEP; ++k) offer(kk[k]);
-        for (int i = p.S + xt + NBR_KEEP * NBR_THREADS; i < n; i += NBR_THREADS) offer(key_at(i));
-        asm volatile("bar.sync 1, %0;" ::"n"(NBR_THREADS) : "memory");
-        __shared__ int s_nbpos[CKV_NEIGHBOURS];
-        if (xw == 0) {
-            const int cnt = s_cnt;
-            int32_t* outn = p.nbr8 ? p.nbr8 + (size_t)u * 8 : nullptr;
-            if (cnt <= 32) {
-                const unsigned long long x = warp_sort_desc(lane < cnt ? s_cand[lane] : 0ull, lane);
-                if (lane < 8) {
-                    const int np = x ? nbr_pos(x) : -1;
-                    s_nbpos[lane] = np;
-                    if (outn) outn[lane] = np;
-                }
-            } else {
-                // many candidates (ties in the logits): 8 rounds, each taking
-                // the best key below the previous winner, from the shared
-                // list or, past its capacity, from the whole list
-                unsigned long long prev = ~0ull;
-                for (int r = 0; r < 8; ++r) {
-                    unsigned long long best = 0;
-                    if (cnt <= NBR_CAP) {
-                        for (int c = lane; c < cnt; c += 32) {
-                            const unsigned long long k2 = s_cand[c];
-                            if (k2 < prev && k2 > best) best = k2;
-                        }
-                    } else {
-                        for (int i = p.S + lane; i < n; i += 32) {
-                            const unsigned long long k2 = key_at(i);
-                            if (k2 < prev && k2 > best) best = k2;
-                        }
-                    }
-                    best = warp_max_u64(best);
-                    if (lane == 0) {
-                        const int np = best ? nbr_pos(best) : -1;
-                        s_nbpos[r] = np;
-                        if (outn) outn[r] = np;
-                    }
-                    prev = best;  // 0 once the entries run out: every later round finds none
-                }
-            }
-        }
-        if (p.append) {
-            asm volatile("bar.sync 1, %0;" ::"n"(NBR_THREADS) : "memory");  // s_nbpos complete
-            merge_assign<T, D, Q8>(p, u, s_nbpos, xt);
-        }
+        search_neighbours<T, D>(p, u, uend - ubeg, t - D);
         return;
     }
 
@@ -358,11 +364,7 @@ __global__ void __launch_bounds__(D + (DENSE ? 0 : 32 * NBR_WARPS), 2) decode_me
       }
     }
 #pragma unroll
-    for (int h = 0; h < GQ; ++h) {
-        // 8-bit cache: a list whose every entry was invalid has no weight
-        if (Q8 && Ls[h] == 0.f) outu[h * D + t] = 0.f;
-        else outu[h * D + t] = A[h] / Ls[h];
-    }
+    for (int h = 0; h < GQ; ++h) outu[h * D + t] = A[h] / Ls[h];
 }
 
 }  // namespace ckv

@@ -44,9 +44,9 @@ struct RowsView {  // new rows in, or read-back rows out
 cudaError_t launch_plan_blocks(const TableView& t, const int32_t* add, const PlanView& p, cudaStream_t st);
 cudaError_t launch_quant_append(const Q8View& c, const PlanView& p, const RowsView& r, cudaStream_t st);
 cudaError_t launch_q8_read(const Q8View& c, const int32_t* first, int R, const RowsView& r, cudaStream_t st);
-// The attention's workspace: counters of the units after the head (of the most there
-// can be, so that they are in the same place for every cache), then the larger of
-// the two calls' partials.
+// The attention's workspace: after the head, counters of the units (of the most there
+// can be, so that they are in the same place for every cache), the partials, and the
+// graph logits of the sparse call's lists.
 constexpr size_t Q8_COUNTER_BYTES = (size_t)MAX_UNITS * 4;
 size_t q8_blocks_ws_bytes(int gq, int d);
 cudaError_t launch_dense_decode_q8(const Q8View& c, const void* q, float* out, void* ws, cudaStream_t st);

@@ -55,6 +55,7 @@ struct BlocksQ8Params {
     int U, G, per_head, tok_cap;
     const int32_t* sel_tok;
     const int32_t* n_tok;
+    float* lam;   // NBR: [U, tok_cap] graph logit of every entry, -inf where it is skipped
     int* count;   // [units], zero between calls
     float* m;     // partials: two slots a block
     float* l;
@@ -204,7 +205,7 @@ __device__ __forceinline__ void copy_half(unsigned sm, const char* k, const char
     }
 }
 
-template <int D, int GQ, int FMT, bool LIST>
+template <int D, int GQ, int FMT, bool LIST, bool NBR>
 __global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_kernel(const __grid_constant__ BlocksQ8Params p) {
     using SH = QdShape<D, LIST>;
     using QG = Q8Geom<D, SH::NH>;
@@ -501,8 +502,16 @@ __global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_
                 if (bad) mask &= ~((bad >> 2 * stage_out & 1u) * 0xffffu | (bad >> 2 * stage_out & 2u) * 0x7fff8000u);
                 left -= QD_WARPS * TOK;
             }
-            st.template tile<!LIST, false>(ring32 + stage_out * QG::SLOT, mask, LIST ? scales[STAGES - 1] : 0.f, lane,
-                                           [](int, float) {});
+            [[maybe_unused]] const int entry0 = (lo + warp + QD_WARPS * x) * TOK;  // the tile's first list entry
+            [[maybe_unused]] float* lamu = NBR ? p.lam + (size_t)b * p.tok_cap + entry0 : nullptr;
+            if constexpr (NBR) {
+                // a tile of skipped entries has no logits of its own to store
+                if (mask == 0u && lane < TOK && entry0 + lane < n) lamu[lane] = -INFINITY;
+            }
+            st.template tile<!LIST, NBR>(ring32 + stage_out * QG::SLOT, mask, LIST ? scales[STAGES - 1] : 0.f, lane,
+                                         [&](int k, float x) {
+                                             if (entry0 + k < n) lamu[k] = x;
+                                         });
             stage_out = stage_out + 1 == STAGES ? 0 : stage_out + 1;
         }
         cp_async_wait<0>();
@@ -552,10 +561,10 @@ __global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_
 }
 
 // Resident blocks, but no more than there can be pieces (`tiles`: the most the units can have).
-template <int D, int GQ, int FMT, bool LIST>
+template <int D, int GQ, int FMT, bool LIST, bool NBR = false>
 static cudaError_t launch_blocks_q8_t(const BlocksQ8Params& p, long long tiles, cudaStream_t st) {
     static LaunchCache lc;
-    auto kern = blocks_q8_kernel<D, GQ, FMT, LIST>;
+    auto kern = blocks_q8_kernel<D, GQ, FMT, LIST, NBR>;
     const size_t smem = BlocksQ8Smem<D, GQ, LIST>::FIXED + (size_t)(LIST ? p.U : p.c.t.B) * 4;
     int per_sm = 0, sms = 0;
     cudaError_t e = prepare_launch(kern, lc, smem, QD_THREADS, &per_sm, &sms);
@@ -565,8 +574,9 @@ static cudaError_t launch_blocks_q8_t(const BlocksQ8Params& p, long long tiles, 
     return launch_pdl(KK_ATTENTION, kern, dim3(grid), dim3(QD_THREADS), smem, st, p);
 }
 
-// The workspace's parts after its head: the units' counters, then the partials.
-inline void carve_blocks_ws(BlocksQ8Params& p, void* ws, int gq) {
+// The workspace's parts after its head: the units' counters, the partials, then the
+// lists' graph logits.
+inline void carve_blocks_ws(BlocksQ8Params& p, void* ws, int gq, int d) {
     char* w = static_cast<char*>(ws) + WS_RESERVED;
     p.count = reinterpret_cast<int*>(w);
     w += Q8_COUNTER_BYTES;
@@ -575,6 +585,8 @@ inline void carve_blocks_ws(BlocksQ8Params& p, void* ws, int gq) {
     p.l = reinterpret_cast<float*>(w);
     w += align256((size_t)2 * QD_MAX_GRID * gq * 4);
     p.acc = reinterpret_cast<float*>(w);
+    w += align256((size_t)2 * QD_MAX_GRID * gq * d * 4);
+    p.lam = reinterpret_cast<float*>(w);
 }
 
 }  // namespace ckv

@@ -16,7 +16,7 @@ cudaError_t launch_dense_decode_q8(const Q8View& c, const void* q, float* out, v
     p.out = out;
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)c.d);
     const int gq = c.Hq / c.Hkv;
-    carve_blocks_ws(p, ws, gq);
+    carve_blocks_ws(p, ws, gq, c.d);
     const long long units = (long long)c.t.B * c.Hkv;
     const long long tiles = units * ((long long)c.t.max_blocks * c.t.block / (QD_MIN_PIECE * 32) + 1);
 #define CKV_QD(DD, GG)                                                                \
