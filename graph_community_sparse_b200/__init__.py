@@ -688,8 +688,10 @@ def ckv_quant_append(cache: Q8Cache, plan: Plan, k_new: torch.Tensor, v_new: tor
         sb, st, sh, _ = _rows(cache, "k_new and v_new", k_new, v_new, (cache.B, T_rows, cache.Hkv, cache.d))
     else:
         raise ValueError("k_new must be [n_rows, Hkv, d] or [B, T, Hkv, d]")
-    if plan.n_rows == 0 or k_new.numel() == 0:
+    if plan.n_rows == 0:
         return
+    if k_new.numel() == 0:
+        raise ValueError("no rows for a plan that has some")
     _call("ckv_quant_append", lib.ckv_quant_append, cache.device, stream, cache.ref, plan.ref, k_new.data_ptr(),
           v_new.data_ptr(), T_rows, sb, st, sh)
 

@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_
                 const int id0 = __shfl_sync(FULL, win_cur, 2 * (x & 15)), id1 = __shfl_sync(FULL, win_cur, 2 * (x & 15) + 1);
                 const int pos = (lo + warp + QD_WARPS * x) * TOK;
                 const bool ok0 = (unsigned)id0 < (unsigned)t.n_blocks, ok1 = (unsigned)id1 < (unsigned)t.n_blocks;
-                const unsigned unit0 = id0 * Hkv + h, unit1 = id1 * Hkv + kvh;
+                const unsigned unit0 = id0 * Hkv + h, unit1 = id1 * Hkv + h;
                 const size_t src0 = (size_t)((unit0 << t.sh) + (pos & (bs - 1))) * D;
                 const size_t src1 = (size_t)((unit1 << t.sh) + ((pos + Q8_HALF) & (bs - 1))) * D;
                 if (pos + TOK <= n && ok0 && ok1) {
@@ -424,7 +424,8 @@ __global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_
         // a window need its positions and their blocks: loaded two and one windows ahead,
         // and only looked at by the copies themselves, so that no load is waited for
         // where it is issued.
-        const int len = LIST ? (int)max(0ll, min((long long)t.len[seq], (long long)t.max_blocks << t.sh)) : 0;
+        int len = LIST ? t.len[seq] : 0;
+        if (LIST && len > (long long)t.max_blocks << t.sh) len = 0;  // a bad length: every entry is out of range
         const int32_t* toks = LIST ? p.sel_tok + (size_t)b * p.tok_cap : nullptr;
         auto entry = [&](int w) {  // of this lane in window w
             return (lo + warp + QD_WARPS * (2 * w + (lane >> 4))) * TOK + (lane & 15);

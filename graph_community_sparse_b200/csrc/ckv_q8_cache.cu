@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(SLOT_THREADS) slots_kernel(const __grid_consta
          r0 += (long long)gridDim.x * SLOT_THREADS * 8) {
         int pos[8], id[8];
         int b = r0 < rows_in ? last_le(s_start, B + 1, (int)r0) : B;
-        int n = 0, n0 = -1;  // the request's length now and before, once looked up
+        int g = 0, n0 = -1;  // tokens granted to the request, and its length before
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int r = (int)r0 + k;
@@ -253,13 +253,13 @@ __global__ void __launch_bounds__(SLOT_THREADS) slots_kernel(const __grid_consta
             if (r0 + k < rows && r < rows_in) {
                 if (n0 < 0 || r >= s_start[b + 1]) {
                     while (r >= s_start[b + 1]) ++b;
-                    n = t.len[b];
-                    n0 = n - max(q.p.granted[b], 0);
+                    g = q.p.granted[b];
+                    n0 = g > 0 ? t.len[b] - g : 0;
                 }
-                const int at = n0 + (r - s_start[b]);
-                if (at < n) {  // else refused
-                    pos[k] = at;
-                    id[k] = t.table[(size_t)b * t.max_blocks + (at >> t.sh)];
+                const int i = r - s_start[b];
+                if (i < g) {  // else refused (a request granted tokens has a good length)
+                    pos[k] = n0 + i;
+                    id[k] = t.table[(size_t)b * t.max_blocks + (pos[k] >> t.sh)];
                 }
             }
         }

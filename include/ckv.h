@@ -508,7 +508,8 @@ CKV_API ckv_status ckv_quant_append(const ckv_q8_desc* cache, const ckv_plan_des
  * rows, or a prefill attention over what is cached.  Row r (0 <= r < R) of
  * request b, head h is position first[b] + r (first NULL: 0) and goes to
  * k_out + b * stride_b + h * stride_h + r * stride_t; positions outside
- * [0, len[b]) give zeros.  16-byte aligned rows; strides in elements.
+ * [0, len[b]) give zeros.  16-byte aligned rows; strides in elements; R <= 2^30,
+ * B * Hkv * R <= 2^36.
  */
 CKV_API ckv_status ckv_q8_read(const ckv_q8_desc* cache, const int32_t* first, int32_t R, void* k_out, void* v_out,
                                int64_t stride_b, int64_t stride_h, int64_t stride_t, ckv_stream_t stream);
@@ -529,7 +530,7 @@ CKV_API ckv_status ckv_q8_workspace_size(const ckv_q8_desc* cache, const ckv_gra
  * queries q [B, Hq, d] (cache dtype, contiguous) over positions [0, len[b]) of
  * each request; out fp32 [B, Hq, d], zeros where len[b] = 0.  Codes are exact
  * in the products, the softmax's statistics and sums are fp32; magnitudes of q
- * below 2^90.  One launch.
+ * below 2^90; B * Hkv * max_blocks * block <= 2^34.  One launch.
  */
 CKV_API ckv_status ckv_dense_decode_q8(const ckv_q8_desc* cache, const void* q, float* out, void* ws, size_t ws_bytes,
                                        ckv_stream_t stream);
@@ -539,7 +540,7 @@ CKV_API ckv_status ckv_dense_decode_q8(const ckv_q8_desc* cache, const void* q, 
  * ckv_score_select, whose cache descriptor then needs shapes only: k = v =
  * NULL, the graph's T_cap) are read through the block table.  out, nbr8 as
  * there; entries outside [0, len[b]) or in a bad block are skipped (and are no
- * neighbours).
+ * neighbours).  One launch, two when nbr8 or k_new is not NULL.
  * k_new [B, Hkv, d] (cache dtype, contiguous) not NULL: the new token, which
  * will be position len[b] of request b, also joins a community of every
  * graph unit as in ckv_sparse_decode_append (same rule and results; assigned

@@ -111,6 +111,7 @@ CASES = [
     ("read R < 0", lambda: _read(rows=-1), INVALID),
     ("read null", lambda: _read(v=None), INVALID),
     ("read misaligned", lambda: _read(k=FAKE + 8), MISALIGNED),
+    ("read R above", lambda: _read(rows=(1 << 30) + 1), UNSUPPORTED),
     ("read overlapping rows", lambda: _read(st=64), INVALID),
     ("dense null q", lambda: _dense(q=None), INVALID),
     ("dense misaligned q", lambda: _dense(q=FAKE + 8), MISALIGNED),
@@ -198,6 +199,7 @@ def test_binding_builds_descriptors():
     lambda c: ckv.ckv_quant_append(c, ckv.new_plan(c, 3), *[torch.zeros(3, 64, dtype=torch.bfloat16)] * 2),
     lambda c: ckv.ckv_quant_append(c, ckv.new_plan(c, 3), torch.zeros(3, 2, 64, dtype=torch.bfloat16),
                                    torch.zeros(2, 3, 64, dtype=torch.bfloat16).transpose(0, 1)),
+    lambda c: ckv.ckv_quant_append(c, ckv.new_plan(c, 3), *[torch.zeros(2, 0, 2, 64, dtype=torch.bfloat16)] * 2),
     lambda c: ckv.ckv_q8_read(c, *[torch.zeros(2, 2, 5, 32, dtype=torch.bfloat16)] * 2),
     lambda c: ckv.ckv_q8_read(c, *[torch.zeros(2, 2, 5, 64, dtype=torch.bfloat16)] * 2, first=torch.zeros(2)),
     lambda c: ckv.ckv_dense_decode_q8(c, torch.zeros(2, 4, 64), torch.zeros(2, 4, 64), torch.zeros(9, dtype=torch.uint8)),

@@ -128,6 +128,21 @@ def test_plan_bad_lengths_are_flagged_and_left():
     assert ckv.ckv_get_device_error(cache, reset=True) == ckv.DEVERR_BLOCK | ckv.DEVERR_PLAN
 
 
+def test_plan_bad_lengths_with_many_rows():
+    """The rows of a request whose length is bad get no slot, lengths next to 2^31 among them."""
+    cache = ckv.new_q8_cache(4, 1, 1, 64, 400, 16, 400)
+    lens = [2 ** 31 - 1, -(2 ** 31), 400 * 16 + 1, 0]
+    cache.len.copy_(i32(lens))
+    p = ckv.new_plan(cache, 12000)
+    ckv.ckv_plan_blocks(cache, i32([3000, 2999, 7, 5000]), p)
+    assert p.granted.tolist() == [0, 0, 0, 5000] and cache.len.tolist() == lens[:3] + [5000]
+    slot = p.slot.tolist()
+    assert slot[:6006] == [-1] * 6006 and slot[11006:] == [-1] * (12000 - 11006)
+    table = cache.table[3].tolist()
+    assert slot[6006:11006] == [table[i // 16] * 16 + i % 16 for i in range(5000)]
+    assert ckv.ckv_get_device_error(cache, reset=True) == ckv.DEVERR_BLOCK | ckv.DEVERR_PLAN
+
+
 # ---------------------------------------------------------------------------
 # append and read
 # ---------------------------------------------------------------------------
@@ -695,6 +710,24 @@ def test_sparse_bad_entries_are_skipped():
     ckv.ckv_sparse_decode_q8(cache, q, graph, sel, out, None, ws)
     assert ckv.ckv_get_device_error(cache, reset=True) == ckv.DEVERR_BLOCK
     check_out(cache, q, out, [good, []])
+
+
+@pytest.mark.parametrize("bad", [-1, 14 * 16 + 1, 2 ** 31 - 1])
+@pytest.mark.parametrize("neighbours", [False, True])
+def test_sparse_bad_length_skips_every_entry(bad, neighbours):
+    cache = filled([200, 50], 1, 4, 64, 16, "int8", torch.bfloat16, seed=7)
+    graph, sel = sparse_state(cache, [list(range(0, 200, 2)), list(range(50))], True, 0, 13 * 16, tok_cap=128)
+    assert cache.desc.blocks.max_blocks == 14
+    q = torch.randn((2, 4, 64), device=DEV).bfloat16()
+    out = torch.full(q.shape, float("nan"), device=DEV)
+    nbr = torch.full((2, 8), -7, dtype=torch.int32, device=DEV) if neighbours else None
+    cache.len[0] = bad
+    ckv.ckv_sparse_decode_q8(cache, q, graph, sel, out, nbr, workspace(cache, graph, sel))
+    assert ckv.ckv_get_device_error(cache, reset=True) == ckv.DEVERR_BLOCK
+    cache.len[0] = 200
+    check_out(cache, q, out, [[], list(range(50))])
+    if neighbours:
+        assert nbr[0].tolist() == [-1] * 8 and min(nbr[1].tolist()) >= 0
 
 
 def test_sparse_joins_communities_like_the_wide_cache():
