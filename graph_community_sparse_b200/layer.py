@@ -31,6 +31,14 @@ def _range(name: str):
         torch.cuda.nvtx.range_pop()
 
 
+def _made_on(stream):
+    """Tensors made inside are allocated and filled on the stream that the calls
+    using them go to."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+
 class LayerState:
     """K, V: [B, Hkv, T_cap, d] device tensors (bf16 or fp32), read in place.
 
@@ -133,7 +141,11 @@ class PagedLayerState:
     it also holds community graphs over positions [0, T_cap): build(), select()
     and attend() are LayerState's, over this cache.  A decode step with graphs is
     select, attend (with the new keys, which join communities), grow, write.
+    grow()'s plan buffers are used again by the next grow() of as many rows; those
+    of more than KEEP_ROWS rows only live until a grow() of another number.
     """
+
+    KEEP_ROWS = 4096
 
     def __init__(self, cache: Q8Cache, mode: str = "group", S: int = 0, Cmax: int = 0, max_tail: int = 0,
                  T_cap: int = 0, tok_cap: Optional[int] = None, rule: str = "score"):
@@ -143,7 +155,7 @@ class PagedLayerState:
         dev = cache.device
         self.out = torch.empty(cache.q_shape, dtype=torch.float32, device=dev)
         self.plan: Optional[Plan] = None
-        self._plans = {}  # by their number of rows: a decode step uses the same one again
+        self._plans = {}  # by their number of rows, up to KEEP_ROWS: a decode step, captured or not, uses the same one again
         self.graph = self.sel = None
         if Cmax > 0:
             self.shape: CacheDesc = q8_shape(cache, T_cap)
@@ -159,8 +171,13 @@ class PagedLayerState:
         """Request b changes by add[b] tokens (int32 [B] on the device); rows
         bounds the tokens that this call may add."""
         plan = self._plans.get(rows)
+        if plan is None and self.plan is not None and self.plan.n_rows == rows:
+            plan = self.plan
         if plan is None:
-            plan = self._plans[rows] = new_plan(self.cache, rows)
+            with _made_on(stream):
+                plan = new_plan(self.cache, rows)
+            if rows <= self.KEEP_ROWS:
+                self._plans[rows] = plan
         with _range("ckv_plan_blocks"):
             ckv_plan_blocks(self.cache, add, plan, stream)
         self.plan = plan
@@ -176,8 +193,9 @@ class PagedLayerState:
     def read(self, R: int, first: Optional[torch.Tensor] = None, stream=None):
         """Positions first[b] .. first[b] + R - 1 of every request as [B, Hkv, R, d] pairs."""
         c = self.cache
-        k = torch.empty((c.B, c.Hkv, R, c.d), dtype=c.dtype, device=c.device)
-        v = torch.empty_like(k)
+        with _made_on(stream):
+            k = torch.empty((c.B, c.Hkv, R, c.d), dtype=c.dtype, device=c.device)
+            v = torch.empty_like(k)
         with _range("ckv_q8_read"):
             ckv_q8_read(c, k, v, first, stream)
         return k, v

@@ -955,3 +955,32 @@ def test_paged_layer_write_follows_grow():
         st.write(torch.zeros((1, 1, 64), dtype=torch.bfloat16, device=DEV), torch.zeros((1, 1, 64), dtype=torch.bfloat16, device=DEV))
     k, v = st.read(5)
     assert k.shape == (1, 1, 5, 64) and (k == 0).all() and (v == 0).all()
+
+
+def test_paged_layer_on_another_stream():
+    """Plans and rows that the layer makes belong to the stream of the call, busy or not current."""
+    from graph_community_sparse_b200.layer import PagedLayerState
+
+    st = PagedLayerState(ckv.new_q8_cache(2, 1, 1, 64, 700, 16, 350, "int8", torch.float32))
+    one, other = i32([1, 1]), i32([5000, 0])
+    rows = torch.randn((2, 5000, 1, 64), device=DEV)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    junk = torch.zeros((1 << 27,), device=DEV)
+    for _ in range(8):
+        junk.add_(1)  # the current stream is behind: what it fills, it fills late
+    small = st.grow(one, 2, s)
+    st.write(rows[:, :1], rows[:, :1], s)
+    large = st.grow(other, 5000, s.cuda_stream)
+    st.write(rows[:, :], rows[:, :], s.cuda_stream)
+    k, v = st.read(5001, stream=s)
+    torch.cuda.synchronize()
+    assert small.granted.tolist() == [1, 1] and large.granted.tolist() == [5000, 0]
+    assert min(small.slot.tolist()) >= 0 and min(large.slot.tolist()) >= 0
+    # half a step of a block's scale (largest magnitude / 127), and the roundings of the code's product; the
+    # first row was re-scaled once, for another half
+    step = float(rows.abs().max()) / 127
+    assert (k[0, 0, 1:] - rows[0, :, 0]).abs().max() <= 0.501 * step
+    assert (k[0, 0, 0] - rows[0, 0, 0]).abs().max() <= 1.002 * step
+    assert torch.equal(k, v)
+    assert st.grow(one, 2, s) is small and st.grow(other, 5000, s) is not large
