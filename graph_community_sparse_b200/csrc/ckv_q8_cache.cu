@@ -354,6 +354,19 @@ __device__ __forceinline__ void vec16_values(const uint4& w, float (&x)[16 / Ele
     }
 }
 
+// The largest magnitude so far, with these values: fp32 bits, or two bf16s, whose
+// order without the sign is that of 16-bit integers.
+template <typename T>
+__device__ __forceinline__ unsigned max_magnitude(unsigned m, const uint4& w) {
+    if constexpr (ElemBytes<T>::v == 2) {
+        constexpr unsigned ABS = 0x7fff7fffu;
+        return __vmaxu2(m, __vmaxu2(__vmaxu2(w.x & ABS, w.y & ABS), __vmaxu2(w.z & ABS, w.w & ABS)));
+    } else {
+        constexpr unsigned ABS = 0x7fffffffu;
+        return max(m, max(max(w.x & ABS, w.y & ABS), max(w.z & ABS, w.w & ABS)));
+    }
+}
+
 template <typename T, int D, int BS, int FMT>
 __global__ void __launch_bounds__(APP_THREADS) append_kernel(const __grid_constant__ AppendParams q) {
     extern __shared__ int s_items[];  // [B + 1] touched blocks before request b
@@ -375,8 +388,10 @@ __global__ void __launch_bounds__(APP_THREADS) append_kernel(const __grid_consta
         const int n = t.len[b], a = q.p.granted[b];
         int x = 0;
         if (a > 0) {
-            const bool ok = n >= a && (long long)n <= (long long)t.max_blocks * BS && q.p.start[b] >= 0 &&
-                            (long long)q.p.start[b] + a <= q.p.n_rows && (q.r.T_rows == 0 || a <= q.r.T_rows);
+            // (rows of their own for every request: the blocks counted here stay within 31 bits)
+            const long long first = q.p.start[b], last = first + a;
+            const bool ok = n >= a && (long long)n <= (long long)t.max_blocks * BS && first >= 0 &&
+                            last <= q.p.n_rows && last <= q.p.start[b + 1] && (q.r.T_rows == 0 || a <= q.r.T_rows);
             if (ok) x = (n - 1) / BS - (n - a) / BS + 1;
             else if (blockIdx.x == 0) atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
         }
@@ -394,14 +409,14 @@ __global__ void __launch_bounds__(APP_THREADS) append_kernel(const __grid_consta
     __syncthreads();
 
     const int r0 = tid / TPR, part = tid % TPR;
-    const long long items = (long long)total * Hkv * 2;
+    const unsigned items = (unsigned)total * Hkv * 2;  // the pool has fewer than 2^31 rows, 16 or more to a block
     struct Item {
         int lo, hi;   // new rows of the block
         int unit;     // block id * Hkv + head; -1: a bad slot
         bool is_v;
     };
-    auto load = [&](long long it, Item& x, uint4 (&w)[NP]) {
-        const int h = (int)((it >> 1) % Hkv), blk_no = (int)((it >> 1) / Hkv);
+    auto load = [&](unsigned it, Item& x, uint4 (&w)[NP]) {
+        const int blk_no = (int)((it >> 1) / (unsigned)Hkv), h = (int)((it >> 1) - (unsigned)blk_no * Hkv);
         const int b = last_le(s_items, B, blk_no);
         const int n = t.len[b], a = q.p.granted[b], start = q.p.start[b];
         const int n_old = n - a;
@@ -430,12 +445,8 @@ __global__ void __launch_bounds__(APP_THREADS) append_kernel(const __grid_consta
         const float s_old = x.lo > 0 ? *scale : 0.f;
         unsigned amax = 0;
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            float y[V];
-            vec16_values<T>(w[p], y);
-#pragma unroll
-            for (int i = 0; i < V; ++i) amax = max(amax, __float_as_uint(y[i]) & 0x7fffffffu);
-        }
+        for (int p = 0; p < NP; ++p) amax = max_magnitude<T>(amax, w[p]);
+        if constexpr (ElemBytes<T>::v == 2) amax = max(amax & 0xffff0000u, amax << 16);
         amax = __reduce_max_sync(FULL, amax);
         if (lane == 0) s_max[warp] = amax;
         __syncthreads();
@@ -474,7 +485,7 @@ __global__ void __launch_bounds__(APP_THREADS) append_kernel(const __grid_consta
         }
         if (tid == 0) *scale = s;
     };
-    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+    for (unsigned it = blockIdx.x; it < items; it += gridDim.x) {
         Item x;
         uint4 w[NP];
         load(it, x, w);
