@@ -333,8 +333,10 @@ cudaError_t launch_plan_blocks(const TableView& t, const int32_t* add, const Pla
 // requests share the grid evenly.
 // ---------------------------------------------------------------------------
 // Small blocks: while some wait at the reduction's barrier, others load (32768 rows
-// of 8 heads: 37 us, 0.82 of the copy rate; 40 with 256 threads, 65 with 512, and
-// 60 with 256 that load their next item ahead, for want of registers).
+// of 8 heads: 34 us, 0.90 of the copy rate; before the instructions an item costs
+// were cut 37, 40 with 256 threads, 65 with 512, and 60 with 256 that load their next
+// item ahead, for want of registers).  One token each of 8 requests: 3.4 us, the
+// launch and the chain length - slot - row - scale.
 constexpr int APP_THREADS = 128;
 
 struct AppendParams {
@@ -527,10 +529,14 @@ cudaError_t launch_quant_append(const Q8View& c, const PlanView& p, const RowsVi
 
 // ---------------------------------------------------------------------------
 // read back.  A thread takes 8 codes of a row (K, then V) for READ_PASS rows,
-// all loads issued before the first is used; bound by the rows written.
+// all loads issued before the first is used; bound by the rows written, few ones by
+// the chain of loads length - block - codes.  32768 rows of 8 heads: 35 us, 0.88 of
+// the copy rate (256 threads of 4 passes 35.8, of 1 pass 37.3; 16 codes a thread 40
+// to 45, whose stores leave half sectors); up to 1000 rows each of 13 requests 5.8 us
+// (7.3 with 256 threads of 4 passes: fewer, longer blocks).
 // ---------------------------------------------------------------------------
-constexpr int READ_THREADS = 256;
-constexpr int READ_PASS = 4;
+constexpr int READ_THREADS = 128;
+constexpr int READ_PASS = 2;
 
 struct ReadParams {
     Q8View c;
