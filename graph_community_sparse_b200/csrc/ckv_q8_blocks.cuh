@@ -11,9 +11,10 @@
 // The second way costs a block that crosses a unit about 12 tiles' time (a new
 // query, an empty ring, a join), the first the difference between the longest
 // piece and the share: the smaller loss decides (33 ragged requests 38.7 us, by ranges
-// 48.6; 8 requests of 128K tokens, whose pieces do not fit, 342, by pieces 355).  (Finer pieces by ticket, for the
-// SMs' 10 % difference in bandwidth, lost more by their starts: 8 requests of
-// 128K tokens 357 against 350 us, 8 heads a group at 64K 249 against 200.)
+// 48.6; 8 requests of 128K tokens, whose pieces do not fit, 342, by pieces 355).
+// (Finer pieces by ticket, for the SMs' 10 % difference in bandwidth, lost more by
+// their starts: 8 requests of 128K tokens 357 against 350 us, 8 heads a group at 64K
+// 249 against 200.)
 //
 // Inside a segment of a unit the warps take tiles in turn, each with its own ring of
 // staged tiles and its own softmax state, joined in shared memory.  A unit that
