@@ -672,6 +672,66 @@ def test_sparse_many_lists_and_long_ones(group, B, n):
     check_out(other, q2, out2)
 
 
+def check_all_tokens(cache, q, out):
+    """check_out's comparison over every token of an fp32 cache, on the GPU in float64."""
+    n = cache.len.long()
+    R = max(int(n.max()), 1)
+    B, Hq, d = q.shape
+    Hkv = cache.desc.Hkv
+    k, v = (torch.empty((B, Hkv, R, d), device=DEV) for _ in range(2))
+    ckv.ckv_q8_read(cache, k, v)
+    k, v, qd = k.double().repeat_interleave(Hq // Hkv, 1), v.double().repeat_interleave(Hq // Hkv, 1), q.double()
+    inside = (torch.arange(R, device=DEV) < n[:, None])[:, None]
+    x = torch.einsum("bhd,bhtd->bht", qd, k) / math.sqrt(d)
+    p = torch.softmax(x.masked_fill(~inside, -math.inf), -1).masked_fill(~inside, 0.0)  # an empty row: NaN, then 0
+    want = torch.einsum("bht,bhtd->bhd", p, v)
+    S = (torch.einsum("bhd,bhtd->bht", qd.abs(), k.abs()) / math.sqrt(d)).amax(-1)
+    rel = 14 * 2.0 ** -23 * S + 3 * 2.0 ** -22 + 2.0 ** -23 * (n[:, None] / 128 + 308)  # Q.attention_tol, and the
+    tol = 4 * rel * v.abs().amax((-1, -2))                                             # read rows' own rounding
+    err = (out.double() - want).abs().amax(-1)
+    assert bool((err <= tol).all()), float((err - tol).max())
+
+
+def test_largest_batch():
+    """8192 requests, the most a table may have: plan, append, dense and sparse attention."""
+    B, gen = 8192, torch.Generator().manual_seed(3)
+    cache = ckv.new_q8_cache(B, 1, 1, 64, 3 * B, 16, 3, "int8", torch.float32)
+    ref = table_lists(cache)
+    lens = torch.randint(0, 49, (B,), generator=gen).tolist()
+    p, _ = plan(cache, ref, lens, sum(lens))
+    k, v = torch.randn((2, sum(lens), 1, 64), generator=gen).to(DEV)
+    ckv.ckv_quant_append(cache, p, k, v)
+    plan(cache, ref, [-(n // 2) if n % 3 else -n for n in lens], 0)
+    assert not all(ref.len) and max(ref.len) < 25
+    q = torch.randn((B, 1, 64), generator=gen).to(DEV)
+    out = torch.full(q.shape, float("nan"), device=DEV)
+    graph, sel = sparse_state(cache, [[]] * B, True, 0, 48, tok_cap=48)
+    sel.sel_tok.copy_(torch.arange(48, dtype=torch.int32, device=DEV).expand(B, 48))
+    sel.n_tok.copy_(cache.len)
+    ws = workspace(cache, graph, sel)
+    ckv.ckv_dense_decode_q8(cache, q, out, ws)
+    check_all_tokens(cache, q, out)
+    nbr = torch.full((B, 8), -7, dtype=torch.int32, device=DEV)
+    for n8 in (None, nbr):
+        out.fill_(float("nan"))
+        ckv.ckv_sparse_decode_q8(cache, q, graph, sel, out, n8, ws)
+        check_all_tokens(cache, q, out)
+    assert torch.equal((nbr >= 0).sum(1), cache.len.clamp(max=8))
+    assert ckv.ckv_get_device_error(cache) == 0
+
+
+@pytest.mark.parametrize("lens", [[65535], [65536], [2048 * 32 + 1, 7], [2047, 2049, 8191, 8192, 8193]])
+def test_dense_lengths_where_the_least_piece_changes(lens):
+    """Units of 64, 256 and 2048 tiles and their neighbours."""
+    cache = filled(lens, 1, 2, 64, 64, "int8", torch.float32, seed=len(lens))
+    q = torch.randn((len(lens), 2, 64), device=DEV)
+    out = torch.full(q.shape, float("nan"), device=DEV)
+    ws = workspace(cache)
+    ckv.ckv_dense_decode_q8(cache, q, out, ws)
+    check_all_tokens(cache, q, out)
+    assert not ws[: 256 + 8192 * 4].any()
+
+
 def test_sparse_all_tokens_equals_dense():
     lens = [300, 77]
     cache = filled(lens, 2, 8, 128, 32, "e4m3", torch.bfloat16, seed=1)
