@@ -27,7 +27,7 @@
 // entries ahead of the copies, and each row brings its own two scales.
 //
 // What bounds it: all tokens, HBM: 8 requests of 128K tokens, 8 heads of 128, in
-// int8 344 to 354 us for 2.15 GB, 0.95 to 0.93 of the copy rate; 4 requests in e4m3
+// int8 336 to 354 us for 2.15 GB, 0.97 to 0.93 of the copy rate; 4 requests in e4m3
 // 177 us, 0.93; d = 64 0.84; 8 query heads a KV head 0.92.  Short work has about 13 us
 // on top of its bytes: the launch, the chain length - block - rows, the join (1
 // request of 32K tokens 24 us, 33 ragged ones up to 9000 tokens 38 us).  Lists: 256 of
