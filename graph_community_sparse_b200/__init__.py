@@ -30,9 +30,9 @@ __all__ = [
     "ASSIGN_SCORE", "ASSIGN_VOTE",
     "DEVERR_SINK_LABEL", "DEVERR_LABEL_RANGE", "DEVERR_TAIL_FULL", "DEVERR_TOKEN_CAP", "DEVERR_INDEX",
     "NEIGHBOURS",
-    "Q8_INT8", "Q8_E4M3", "DEVERR_PLAN", "DEVERR_BLOCK", "TableDesc", "Q8Desc", "PlanDesc", "BlockTable", "Q8Cache",
+    "Q8_INT8", "Q8_E4M3", "DEVERR_PLAN", "DEVERR_BLOCK", "DEVERR_CUT", "TableDesc", "Q8Desc", "PlanDesc", "BlockTable", "Q8Cache",
     "Plan", "block_table", "q8_cache", "new_q8_cache", "new_plan", "q8_shape", "ckv_plan_blocks", "ckv_quant_append",
-    "ckv_q8_read", "ckv_q8_workspace_size", "ckv_dense_decode_q8", "ckv_sparse_decode_q8",
+    "ckv_q8_read", "ckv_q8_workspace_size", "ckv_dense_decode_q8", "ckv_sparse_decode_q8", "ckv_trim_graph_q8",
 ]
 
 # the in-tree build, always: no environment variable selects another library
@@ -46,7 +46,7 @@ PER_GROUP, PER_HEAD = 0, 1
 ASSIGN_SCORE, ASSIGN_VOTE = 0, 1
 DEVERR_SINK_LABEL, DEVERR_LABEL_RANGE, DEVERR_TAIL_FULL, DEVERR_TOKEN_CAP, DEVERR_INDEX = 1, 2, 4, 8, 16
 DEVERR_EDGE_CAP = 32
-DEVERR_PLAN, DEVERR_BLOCK = 64, 128
+DEVERR_PLAN, DEVERR_BLOCK, DEVERR_CUT = 64, 128, 256
 Q8_INT8, Q8_E4M3 = 0, 1
 NEIGHBOURS = 8
 KERNEL_KINDS = ("build", "score", "select", "attention", "merge", "update", "edges")
@@ -56,7 +56,7 @@ EXPORTED = ("ckv_workspace_size", "ckv_build_centroids", "ckv_score_select", "ck
             "ckv_dense_decode",
             "ckv_edges_workspace_size", "ckv_build_edges",
             "ckv_plan_blocks", "ckv_quant_append", "ckv_q8_read", "ckv_q8_workspace_size", "ckv_dense_decode_q8",
-            "ckv_sparse_decode_q8",
+            "ckv_sparse_decode_q8", "ckv_trim_graph_q8",
             "ckv_status_string", "ckv_last_error", "ckv_abi_version", "ckv_debug_build")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -84,7 +84,7 @@ class GraphDesc(ctypes.Structure):
     _fields_ = [("mode", _i32), ("S", _i32), ("Cmax", _i32), ("max_tail", _i32), ("T_cap", _i32),
                 ("assign_rule", _i32), ("comm_of", _p), ("offs", _p), ("tok", _p), ("cnt", _p), ("cent", _p), ("cent_q", _p), ("cent_qs", _p),
                 ("num_comm", _p), ("tail_tok", _p), ("tail_comm", _p), ("tail_len", _p),
-                ("dev_err", _p)]
+                ("dev_err", _p), ("undo", _p), ("built", _p)]
 
 
 class SelectionDesc(ctypes.Structure):
@@ -131,6 +131,7 @@ def _declare(lib_: ctypes.CDLL) -> ctypes.CDLL:
     lib_.ckv_dense_decode_q8.argtypes = [_P(Q8Desc), _p, _p, _p, _sz, _p]
     lib_.ckv_sparse_decode_q8.argtypes = [_P(Q8Desc), _p, _P(GraphDesc), _P(SelectionDesc), _p, _p, _p, _p, _p, _sz,
                                           _p]
+    lib_.ckv_trim_graph_q8.argtypes = [_P(Q8Desc), _P(GraphDesc), _p]
     lib_.ckv_get_device_error.argtypes = [_P(GraphDesc), _p, _P(ctypes.c_int32), _i32]
     lib_.ckv_kernel_timing.argtypes = [_i32]
     lib_.ckv_kernel_times.argtypes = [_P(ctypes.c_float), _P(ctypes.c_int32), _i32]
@@ -138,7 +139,7 @@ def _declare(lib_: ctypes.CDLL) -> ctypes.CDLL:
               "ckv_sparse_decode_noalloc", "ckv_assign_update", "ckv_append_assign", "ckv_sparse_decode_append",
               "ckv_dense_decode", "ckv_get_device_error", "ckv_kernel_timing", "ckv_kernel_times",
               "ckv_edges_workspace_size", "ckv_build_edges", "ckv_plan_blocks", "ckv_quant_append", "ckv_q8_read",
-              "ckv_q8_workspace_size", "ckv_dense_decode_q8", "ckv_sparse_decode_q8"):
+              "ckv_q8_workspace_size", "ckv_dense_decode_q8", "ckv_sparse_decode_q8", "ckv_trim_graph_q8"):
         getattr(lib_, f).restype = ctypes.c_int
     lib_.ckv_status_string.argtypes = [ctypes.c_int]
     lib_.ckv_status_string.restype = ctypes.c_char_p
@@ -235,6 +236,8 @@ class Graph:
     tail_comm: torch.Tensor
     tail_len: torch.Tensor
     dev_err: torch.Tensor
+    undo: Optional[torch.Tensor] = None
+    built: Optional[torch.Tensor] = None
 
     @property
     def U(self) -> int:
@@ -254,7 +257,9 @@ class Selection:
 
 
 def new_graph(cache: CacheDesc, mode: int, S: int, Cmax: int, max_tail: int, device="cuda",
-              rule: int = ASSIGN_SCORE) -> Graph:
+              rule: int = ASSIGN_SCORE, undo: bool = False) -> Graph:
+    """undo: with room to take tail members out again (fp32 [U, max_tail, d]), which a paged 8-bit cache's
+    requests need when they lose tokens."""
     G = cache.Hq if mode == PER_HEAD else cache.Hkv
     U = cache.B * G
     i32 = dict(dtype=torch.int32, device=device)
@@ -271,10 +276,13 @@ def new_graph(cache: CacheDesc, mode: int, S: int, Cmax: int, max_tail: int, dev
         tail_comm=torch.zeros((U, max(max_tail, 1)), **i32),
         tail_len=torch.zeros((U,), **i32),
         dev_err=torch.zeros((1,), **i32),
+        built=torch.zeros((U,), **i32),
     )
+    if undo:
+        t["undo"] = torch.zeros((U, max(max_tail, 1), cache.d), dtype=torch.float32, device=device)
     desc = GraphDesc(mode, S, Cmax, max_tail, cache.T_cap, rule, *(t[k].data_ptr() for k in (
         "comm_of", "offs", "tok", "cnt", "cent", "cent_q", "cent_qs", "num_comm", "tail_tok", "tail_comm", "tail_len",
-        "dev_err")))
+        "dev_err")), _ptr(t.get("undo")), t["built"].data_ptr())
     return Graph(desc, **t)
 
 
@@ -747,3 +755,13 @@ def ckv_sparse_decode_q8(cache: Q8Cache, q: torch.Tensor, graph: Graph, sel: Sel
     ap = None if assigned is None else _need("assigned", assigned, torch.int32, (graph.U,), dev)
     _call("ckv_sparse_decode_q8", lib.ckv_sparse_decode_q8, dev, stream, cache.ref, qp, ctypes.byref(graph.desc),
           ctypes.byref(sel.desc), op, np_, kp, ap, ws.data_ptr(), ws.numel())
+
+
+def ckv_trim_graph_q8(cache: Q8Cache, graph: Graph, stream=None) -> None:
+    """Takes the tokens at or past each request's length out of its communities: after a ckv_plan_blocks that may have
+    refused a joined token or dropped tokens, before the next ckv_score_select.  The graph needs new_graph(undo=True)."""
+    dev = cache.device
+    U = cache.B * (cache.Hq if graph.desc.mode == PER_HEAD else cache.Hkv)
+    if graph.U != U or graph.dev_err.device != dev:
+        raise ValueError("the graph must be for this cache's batch and heads, on its device")
+    _call("ckv_trim_graph_q8", lib.ckv_trim_graph_q8, dev, stream, cache.ref, ctypes.byref(graph.desc))

@@ -146,6 +146,8 @@ ckv::GraphView graph_view(const ckv_cache_desc* c, const ckv_graph_desc* g) {
     v.tail_comm = g->tail_comm;
     v.tail_len = g->tail_len;
     v.dev_err = g->dev_err;
+    v.undo = g->undo;
+    v.built = g->built;
     return v;
 }
 
@@ -616,6 +618,17 @@ ckv_status ckv_sparse_decode_q8(const ckv_q8_desc* cache, const void* q, const c
     return cuda_status(ckv::launch_sparse_decode_q8(q8_view(cache), graph_view(&shape, graph), sel_view(sel), q, out,
                                                     nbr8, k_new, assigned, ws, reinterpret_cast<cudaStream_t>(stream)),
                        "ckv_sparse_decode_q8");
+}
+
+ckv_status ckv_trim_graph_q8(const ckv_q8_desc* cache, const ckv_graph_desc* graph, ckv_stream_t stream) {
+    CKV_TRY(check_q8(cache));
+    CKV_TRY(check_q8_graph(cache, graph));
+    if (!graph->built || (graph->max_tail > 0 && !graph->undo))
+        return fail(CKV_ERR_INVALID_ARG, "the graph has no undo or built array");
+    const ckv_cache_desc shape = q8_shape(cache, graph->T_cap);
+    return cuda_status(ckv::launch_trim_graph_q8(q8_view(cache), graph_view(&shape, graph),
+                                                 reinterpret_cast<cudaStream_t>(stream)),
+                       "ckv_trim_graph_q8");
 }
 
 }  // extern "C"

@@ -43,6 +43,7 @@ struct AssignParams {
     int32_t* tail_len;
     int32_t* dev_err;
     int32_t* assigned;
+    float* undo;        // [U, max_tail, d] or NULL: a tail member's centre before it joined
 };
 
 // Fills the fields that come from the cache, the graph and the call.
@@ -91,6 +92,7 @@ inline AssignParams make_assign_params(const CacheView& c, const GraphView& g, i
     p.tail_len = g.tail_len;
     p.dev_err = g.dev_err;
     p.assigned = assigned;
+    p.undo = g.undo;
     return p;
 }
 
@@ -128,14 +130,33 @@ __device__ __forceinline__ void append_rows(const AssignParams& p, int u, int t,
     }
 }
 
+// The int8 scoring copy of centre row `rowi`, of which this lane holds E elements
+// (amax: their largest magnitude): new scale, new codes.  One warp.
+template <int D>
+__device__ __forceinline__ void write_scoring_copy(const AssignParams& p, size_t rowi, const float (&c)[D / 32],
+                                                   float amax, int lane) {
+    constexpr int E = D / 32;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, o));
+    const float scl = q8_scale(amax), rc = q8_recip(amax);
+    uint32_t packed = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) packed |= (uint32_t)(q8_code(c[e], rc) & 0xff) << (8 * e);
+    int8_t* qr = p.cent_q + rowi * D + lane * E;
+    if constexpr (E == 4) *reinterpret_cast<uint32_t*>(qr) = packed;
+    else *reinterpret_cast<uint16_t*>(qr) = (uint16_t)packed;
+    if (lane == 0) p.cent_qs[rowi] = scl;
+}
+
 // The update of unit u by NW warps (thread index tid in [0, 32 NW)), given
 // the unit's 8 neighbour positions (-1: none) in nbrpos, readable by all of
 // them.  sync() is a barrier over exactly these NW warps.  Warp w scores
 // candidates w, w + NW, ... with all of their centres requested before any
 // is used; warp 0 picks the winner and moves its centre.  APPEND: the last
 // warp also writes the new K/V rows (append_rows; the attention's merge
-// kernel does that itself, off the update's path).
-template <typename T, int D, int NW, bool APPEND, typename Sync>
+// kernel does that itself, off the update's path).  UNDO: the winner's centre
+// as it was is kept in p.undo, where there is one.
+template <typename T, int D, int NW, bool APPEND, bool UNDO = false, typename Sync>
 __device__ __forceinline__ void assign_unit(const AssignParams& p, int u, const int* nbrpos, int tid,
                                             AssignScratch<D>& sc, Sync sync) {
     constexpr int E = D / 32;
@@ -261,6 +282,13 @@ __device__ __forceinline__ void assign_unit(const AssignParams& p, int u, const 
     const float* c0r = sc.row[bi] + lane * E;
     const float inv_n1 = __frcp_rn((float)(n + 1));  // one reciprocal, then products
     float c1[E], amax = 0.f;
+    if constexpr (UNDO) {
+        if (p.undo) {
+            float* un = p.undo + ((size_t)u * p.max_tail + tl) * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; ++e) un[e] = c0r[e];
+        }
+    }
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         const float c0 = c0r[e];
@@ -269,16 +297,40 @@ __device__ __forceinline__ void assign_unit(const AssignParams& p, int u, const 
         amax = fmaxf(amax, fabsf(c1[e]));
     }
     // the int8 scoring copy follows the centre: new scale, new codes
+    write_scoring_copy<D>(p, rowi, c1, amax, lane);
+}
+
+// Takes the tail members of unit u at positions >= len out again, last first,
+// and leaves the unit as it was before they joined, bit for bit: the count,
+// comm_of, the centre (from p.undo, not NULL) and its scoring copy, which is a
+// function of the centre.  Positions join in ascending order, so these
+// members are the tail's end.  One warp.
+template <int D>
+__device__ __forceinline__ void untail_unit(const AssignParams& p, int u, int len, int lane) {
+    constexpr int E = D / 32;
+    const size_t row0 = (size_t)u * p.max_tail;
+    const int tl = min(p.tail_len[u], p.max_tail);
+    int n = tl;
+    for (; n > 0; --n) {
+        const size_t at = row0 + n - 1;
+        const int pos = p.tail_tok[at], c = p.tail_comm[at];
+        if (pos < len) break;
+        if (c < 0 || c >= p.Cmax) continue;  // not written by a join
+        const size_t rowi = (size_t)u * p.Cmax + c;
+        float c0[E], amax = 0.f;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, o));
-    const float scl = q8_scale(amax), rc = q8_recip(amax);
-    uint32_t packed = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) packed |= (uint32_t)(q8_code(c1[e], rc) & 0xff) << (8 * e);
-    int8_t* qr = p.cent_q + rowi * D + lane * E;
-    if constexpr (E == 4) *reinterpret_cast<uint32_t*>(qr) = packed;
-    else *reinterpret_cast<uint16_t*>(qr) = (uint16_t)packed;
-    if (lane == 0) p.cent_qs[rowi] = scl;
+        for (int e = 0; e < E; ++e) {
+            c0[e] = p.undo[at * D + lane * E + e];
+            p.cent[rowi * D + lane * E + e] = c0[e];
+            amax = fmaxf(amax, fabsf(c0[e]));
+        }
+        write_scoring_copy<D>(p, rowi, c0, amax, lane);
+        if (lane == 0) {
+            p.cnt[rowi] -= 1;
+            if (pos < p.T_cap) p.comm_of[(size_t)u * p.T_cap + pos] = -1;
+        }
+    }
+    if (lane == 0 && n < tl) p.tail_len[u] = n;
 }
 
 }  // namespace ckv

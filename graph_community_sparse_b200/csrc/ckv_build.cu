@@ -38,6 +38,7 @@ struct BuildParams {
     int32_t* num_comm;
     int32_t* tail_len;
     int32_t* dev_err;
+    int32_t* built;  // may be NULL
 };
 
 __global__ void __launch_bounds__(256) build_hist(BuildParams p) {
@@ -102,6 +103,7 @@ __global__ void __launch_bounds__(1024) build_scan(BuildParams p) {
         p.offs[(size_t)u * (p.Cmax + 1) + p.Cmax] = carry;
         p.num_comm[u] = s_maxc + 1;
         p.tail_len[u] = 0;
+        if (p.built) p.built[u] = p.T;
     }
 }
 
@@ -222,6 +224,7 @@ cudaError_t launch_build(const CacheView& c, const GraphView& g, const int32_t* 
     p.num_comm = g.num_comm;
     p.tail_len = g.tail_len;
     p.dev_err = g.dev_err;
+    p.built = g.built;
     const int U = c.B * g.G;
     const size_t hsm = (size_t)g.Cmax * 4;
     static LaunchCache lc_hist, lc_scatter;

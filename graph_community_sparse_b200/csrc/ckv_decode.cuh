@@ -67,6 +67,7 @@ struct DecodeParams {
     int append;             // fused community update (and K/V append) in the merge
     AssignParams ap;
     const int32_t* len;     // 8-bit cache: tokens per request, the position each request's new token joins at
+    const int32_t* built;   // 8-bit cache: positions each unit was built over, or NULL
 };
 
 __device__ __forceinline__ void unit_heads(const DecodeParams& p, int u, int gq, bool dense,
@@ -112,25 +113,42 @@ __device__ __forceinline__ int nbr_pos(unsigned long long k) {
     return 0x7fffffff - (int)(unsigned)(k & 0xffffffffu);
 }
 
+// An 8-bit cache's unit before its new token joins: the request's length, the last
+// tail member's position (-1: none) and the positions the unit was built over.
+// Loaded ahead of the neighbour search, looked at after it.
+struct JoinAt {
+    int len = 0, last = -1, built = 0;
+};
+
 // The fused community update of unit u by the merge block's NBR_WARPS
 // neighbour warps (thread xt of 32 NBR_WARPS), given its neighbour positions.
 template <typename T, int D, bool Q8 = false>
-__device__ __forceinline__ void merge_assign(const DecodeParams& p, int u, const int* nbpos, int xt) {
+__device__ __forceinline__ void merge_assign(const DecodeParams& p, int u, const int* nbpos, int xt,
+                                             const JoinAt& at = JoinAt()) {
     __shared__ __align__(16) AssignScratch<D> s_as;
     auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(NBR_THREADS) : "memory"); };
     if constexpr (Q8) {
         // the requests of an 8-bit cache differ in length: each one's token
-        // joins at its own end
+        // joins at its own end.  A position joins once: members at it or past it
+        // (growth refused since, or tokens given back) leave first.
         AssignParams ap = p.ap;
-        ap.pos = p.len[u / p.G];
-        if (ap.pos < 0 || ap.pos >= ap.T_cap) {
+        ap.pos = at.len;
+        const bool stale = at.last >= ap.pos;
+        const int err = ap.pos < 0 || ap.pos >= ap.T_cap || (stale && !ap.undo) ? CKV_DEVERR_INDEX
+                        : ap.pos < at.built                                     ? CKV_DEVERR_CUT
+                                                                                : 0;
+        if (err) {
             if (xt == 0) {
-                atomicOr(ap.dev_err, CKV_DEVERR_INDEX);
+                atomicOr(ap.dev_err, err);
                 if (ap.assigned) ap.assigned[u] = -1;
             }
             return;
         }
-        assign_unit<T, D, NBR_WARPS, false>(ap, u, nbpos, xt, s_as, sync);
+        if (stale) {
+            if (xt < 32) untail_unit<D>(ap, u, ap.pos, xt);
+            sync();
+        }
+        assign_unit<T, D, NBR_WARPS, false, true>(ap, u, nbpos, xt, s_as, sync);
     } else {
         assign_unit<T, D, NBR_WARPS, false>(p.ap, u, nbpos, xt, s_as, sync);
     }
@@ -139,7 +157,8 @@ __device__ __forceinline__ void merge_assign(const DecodeParams& p, int u, const
 // The neighbours of unit u, a list of n >= 1 entries, and its fused update, by
 // NBR_THREADS threads (xt of them).
 template <typename T, int D, bool Q8 = false>
-__device__ __forceinline__ void search_neighbours(const DecodeParams& p, int u, int n, int xt) {
+__device__ __forceinline__ void search_neighbours(const DecodeParams& p, int u, int n, int xt,
+                                                  const JoinAt& at = JoinAt()) {
     // neighbour search over the graph logits the attention kernel stored,
     // for the unit's non-sink list entries [S, n).  Threshold filter:
     // theta = the 8th largest of the NBR_THREADS per-thread maxima is a
@@ -234,7 +253,7 @@ __device__ __forceinline__ void search_neighbours(const DecodeParams& p, int u, 
     }
     if (p.append) {
         asm volatile("bar.sync 1, %0;" ::"n"(NBR_THREADS) : "memory");  // s_nbpos complete
-        merge_assign<T, D, Q8>(p, u, s_nbpos, xt);
+        merge_assign<T, D, Q8>(p, u, s_nbpos, xt, at);
     }
 }
 

@@ -258,6 +258,8 @@ struct GraphView {
     int32_t* tail_comm;
     int32_t* tail_len;
     int32_t* dev_err;
+    float* undo;     // [U, max_tail, d] or NULL
+    int32_t* built;  // [U] or NULL
 };
 
 struct SelView {

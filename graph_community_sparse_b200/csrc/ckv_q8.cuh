@@ -52,6 +52,7 @@ size_t q8_blocks_ws_bytes(int gq, int d);
 cudaError_t launch_dense_decode_q8(const Q8View& c, const void* q, float* out, void* ws, cudaStream_t st);
 cudaError_t launch_sparse_decode_q8(const Q8View& c, const GraphView& g, const SelView& s, const void* q, float* out,
                                     int32_t* nbr8, const void* k_new, int32_t* assigned, void* ws, cudaStream_t st);
+cudaError_t launch_trim_graph_q8(const Q8View& c, const GraphView& g, cudaStream_t st);
 
 // ---------------------------------------------------------------------------
 // formats.  int8: scale amax/127.  e4m3: a power-of-two scale, which costs a

@@ -17,16 +17,78 @@ __global__ void __launch_bounds__(NBR_THREADS) neighbours_q8_kernel(const __grid
     pdl_wait();  // the logits are complete and visible
     const int u = blockIdx.x, t = threadIdx.x;
     const int n = max(0, min(p.n_tok[u], p.tok_cap));
+    JoinAt at;
+    if (p.append) {
+        at.len = p.len[u / p.G];
+        if (p.built) at.built = p.built[u];
+        const int tl = min(p.ap.tail_len[u], p.ap.max_tail);
+        if (tl > 0) at.last = p.ap.tail_tok[(size_t)u * p.ap.max_tail + tl - 1];
+    }
     if (n > 0) {
-        search_neighbours<T, D, true>(p, u, n, t);
+        search_neighbours<T, D, true>(p, u, n, t, at);
         return;
     }
     if (p.nbr8 && t < CKV_NEIGHBOURS) p.nbr8[(size_t)u * CKV_NEIGHBOURS + t] = -1;
     if (p.append) {
         __shared__ int s_none[CKV_NEIGHBOURS];
         if (t < CKV_NEIGHBOURS) s_none[t] = -1;
-        merge_assign<T, D, true>(p, u, s_none, t);  // no neighbour: the token joins nothing
+        merge_assign<T, D, true>(p, u, s_none, t, at);  // no neighbour: the token joins nothing
     }
+}
+
+// A graph after its requests' lengths went down, or did not go up as a join
+// expected (ckv_trim_graph_q8): a block per unit.  Nothing to do is the rule: 2
+// dependent loads.
+constexpr int TRIM_THREADS = 128;
+
+struct TrimParams {
+    TableView t;
+    AssignParams ap;
+    int32_t* offs;
+    int32_t* num_comm;
+    int32_t* built;
+};
+
+template <int D>
+__global__ void __launch_bounds__(TRIM_THREADS) trim_graph_kernel(const __grid_constant__ TrimParams p) {
+    pdl_wait();
+    const AssignParams& ap = p.ap;
+    const int u = blockIdx.x, tid = threadIdx.x;
+    const int n = p.t.len[u / ap.G], built = p.built[u];
+    if (n < 0 || n > (long long)p.t.max_blocks << p.t.sh) {
+        if (tid == 0) atomicOr(p.t.dev_err, CKV_DEVERR_BLOCK);
+        return;
+    }
+    if (n >= built) {
+        if (tid < 32) untail_unit<D>(ap, u, n, tid);
+        return;
+    }
+    // members of the build are gone: their communities cannot be kept
+    for (int i = tid; i < ap.Cmax; i += TRIM_THREADS) {
+        ap.cnt[(size_t)u * ap.Cmax + i] = 0;
+        p.offs[(size_t)u * (ap.Cmax + 1) + i + 1] = 0;
+    }
+    for (int i = tid; i < ap.T_cap; i += TRIM_THREADS) ap.comm_of[(size_t)u * ap.T_cap + i] = -1;
+    __syncthreads();  // everybody has read built
+    if (tid == 0) {
+        p.num_comm[u] = 0;
+        ap.tail_len[u] = 0;
+        p.built[u] = 0;
+        if (n > 0) atomicOr(ap.dev_err, CKV_DEVERR_CUT);
+    }
+}
+
+cudaError_t launch_trim_graph_q8(const Q8View& c, const GraphView& g, cudaStream_t st) {
+    CacheView v{};
+    v.B = c.t.B;
+    v.Hkv = c.Hkv;
+    v.Hq = c.Hq;
+    v.d = c.d;
+    v.dtype = c.dtype;
+    const TrimParams p{c.t, make_assign_params(v, g, 0, nullptr, nullptr, nullptr, nullptr), g.offs, g.num_comm, g.built};
+    const dim3 grid(p.ap.U), block(TRIM_THREADS);
+    if (c.d == 128) return launch_pdl(KK_UPDATE, trim_graph_kernel<128>, grid, block, 0, st, p);
+    return launch_pdl(KK_UPDATE, trim_graph_kernel<64>, grid, block, 0, st, p);
 }
 
 template <int D, int GQ, int FMT>
@@ -65,6 +127,7 @@ cudaError_t launch_sparse_decode_q8(const Q8View& c, const GraphView& g, const S
     d.want_nbr = nbr8 != nullptr || k_new != nullptr;
     d.nbr8 = nbr8;
     d.len = c.t.len;
+    d.built = g.built;
     if (k_new) {
         CacheView v{};
         v.B = c.t.B;

@@ -17,7 +17,7 @@ from . import (ASSIGN_SCORE, ASSIGN_VOTE, PER_GROUP, PER_HEAD, Graph, Selection,
                ckv_build_centroids, ckv_dense_decode, ckv_score_select, ckv_sparse_decode,
                ckv_workspace_size, new_graph, new_selection, new_workspace, NEIGHBOURS,
                CacheDesc, Plan, Q8Cache, ckv_dense_decode_q8, ckv_plan_blocks, ckv_q8_read, ckv_q8_workspace_size,
-               ckv_quant_append, ckv_sparse_decode_q8, new_plan, q8_shape)
+               ckv_quant_append, ckv_sparse_decode_q8, ckv_trim_graph_q8, new_plan, q8_shape)
 
 
 @contextlib.contextmanager
@@ -141,6 +141,9 @@ class PagedLayerState:
     it also holds community graphs over positions [0, T_cap): build(), select()
     and attend() are LayerState's, over this cache.  A decode step with graphs is
     select, attend (with the new keys, which join communities), grow, write.
+    Joins are undone by the grow() that refuses their token, adds none, or gives
+    it back later; a request that falls below the positions its communities were
+    built over loses them (DEVERR_CUT, unless it ended) until the next build().
     grow()'s plan buffers are used again by the next grow() of as many rows; those
     of more than KEEP_ROWS rows only live until a grow() of another number.
     """
@@ -160,7 +163,7 @@ class PagedLayerState:
         if Cmax > 0:
             self.shape: CacheDesc = q8_shape(cache, T_cap)
             self.graph = new_graph(self.shape, PER_HEAD if mode == "head" else PER_GROUP, S, Cmax, max_tail, device=dev,
-                                   rule=ASSIGN_VOTE if rule == "vote" else ASSIGN_SCORE)
+                                   rule=ASSIGN_VOTE if rule == "vote" else ASSIGN_SCORE, undo=True)
             self.sel = new_selection(self.shape, self.graph, tok_cap or T_cap, device=dev)
             self.nbr8 = torch.full((self.graph.U, NEIGHBOURS), -1, dtype=torch.int32, device=dev)
             self.assigned = torch.full((self.graph.U,), -1, dtype=torch.int32, device=dev)
@@ -169,7 +172,7 @@ class PagedLayerState:
 
     def grow(self, add: torch.Tensor, rows: int, stream=None) -> Plan:
         """Request b changes by add[b] tokens (int32 [B] on the device); rows
-        bounds the tokens that this call may add."""
+        bounds the tokens that this call may add.  The graphs follow."""
         plan = self._plans.get(rows)
         if plan is None and self.plan is not None and self.plan.n_rows == rows:
             plan = self.plan
@@ -181,6 +184,9 @@ class PagedLayerState:
         with _range("ckv_plan_blocks"):
             ckv_plan_blocks(self.cache, add, plan, stream)
         self.plan = plan
+        if self.graph is not None:
+            with _range("ckv_trim_graph_q8"):
+                ckv_trim_graph_q8(self.cache, self.graph, stream)
         return plan
 
     def write(self, k_new: torch.Tensor, v_new: torch.Tensor, stream=None) -> None:

@@ -65,7 +65,7 @@ extern "C" {
 #define CKV_API
 #endif
 
-#define CKV_ABI_VERSION 8
+#define CKV_ABI_VERSION 9
 #define CKV_NEIGHBOURS 8
 
 typedef struct CUstream_st* ckv_stream_t; /* the same handle as cudaStream_t */
@@ -105,6 +105,8 @@ typedef enum { CKV_ASSIGN_SCORE = 0, CKV_ASSIGN_VOTE = 1 } ckv_assign_rule;
 #define CKV_DEVERR_PLAN 64        /* ckv_plan_blocks refused a request's growth (granted = 0)          */
 #define CKV_DEVERR_BLOCK 128      /* 8-bit cache: a length, a slot or a block id of the table was
                                      out of range (checked in every build); its tokens were skipped   */
+#define CKV_DEVERR_CUT 256        /* 8-bit cache: a request fell below the positions its graph was built
+                                     over; the graph was emptied, or the token not joined           */
 #define CKV_DEVERR_INDEX 16       /* debug builds: an index read from a caller's array
                                      (a position, a run offset, a token count, a tail
                                      length) was out of range; the access was skipped */
@@ -146,6 +148,13 @@ typedef struct {
  *   tail_tok, tail_comm int32 [U, max_tail]  tokens joined after the build
  *   tail_len int32 [U]
  *   dev_err  int32 [1]          OR of CKV_DEVERR_* bits; the caller zeroes it
+ *   undo     fp32  [U, max_tail, d] or NULL: the centre of its community before
+ *                  each tail member joined, kept by ckv_sparse_decode_q8 so that
+ *                  the member can be taken out again
+ *   built    int32 [U] or NULL  positions [0, built) were labelled when the unit
+ *                  was built (0: never); written by the builds
+ * undo and built are for the graphs of a paged 8-bit cache, whose requests can
+ * lose tokens (ckv_trim_graph_q8); the other calls leave undo alone.
  * assign_rule is a ckv_assign_rule; any other value is CKV_ERR_INVALID_ARG.
  * S sink positions 0..S-1 belong to no community and are always attended
  * ([R-A] paragraph 3).  T_cap here must equal the cache's T_cap.
@@ -169,6 +178,8 @@ typedef struct {
     int32_t* tail_comm;
     int32_t* tail_len;
     int32_t* dev_err;
+    float* undo;        /* [U, max_tail, d] or NULL */
+    int32_t* built;     /* [U] or NULL */
 } ckv_graph_desc;
 
 /*
@@ -545,12 +556,31 @@ CKV_API ckv_status ckv_dense_decode_q8(const ckv_q8_desc* cache, const void* q, 
  * will be position len[b] of request b, also joins a community of every
  * graph unit as in ckv_sparse_decode_append (same rule and results; assigned
  * as there); its rows are then written by ckv_plan_blocks and
- * ckv_quant_append.  A request with len[b] >= T_cap joins nothing
- * (CKV_DEVERR_INDEX).  graph->T_cap <= max_blocks * block.
+ * ckv_quant_append.  Where that growth is refused, is of no token, or tokens are
+ * dropped later, ckv_trim_graph_q8 takes the token out of its communities again.
+ * A position joins once: tail members at or past len[b] leave first, in the same
+ * way; without graph->undo the token joins nothing instead (CKV_DEVERR_INDEX).
+ * A request with len[b] >= T_cap joins nothing (CKV_DEVERR_INDEX), nor does one
+ * below the positions its graph was built over (CKV_DEVERR_CUT).  A call joins
+ * one token a request; tokens written without a join belong to no community.
+ * graph->T_cap <= max_blocks * block.
  */
 CKV_API ckv_status ckv_sparse_decode_q8(const ckv_q8_desc* cache, const void* q, const ckv_graph_desc* graph,
                                         const ckv_selection_desc* sel, float* out, int32_t* nbr8, const void* k_new,
                                         int32_t* assigned, void* ws, size_t ws_bytes, ckv_stream_t stream);
+
+/*
+ * Brings a graph in step with the lengths that ckv_plan_blocks left: call it
+ * after a ckv_plan_blocks that may refuse a joined token or drop tokens, before the
+ * next ckv_score_select.  In every graph unit of request b the tail members at
+ * positions >= len[b] leave, last first; counts, comm_of, centres and their scoring
+ * copies are then, bit for bit, what they were before those members joined.  A
+ * unit built over more than len[b] positions is emptied (no community, no member;
+ * its selection is the sinks alone until it is built again), with CKV_DEVERR_CUT
+ * unless len[b] is 0.  A request with a bad length is left as it is
+ * (CKV_DEVERR_BLOCK).  graph->undo and graph->built are needed.  One launch.
+ */
+CKV_API ckv_status ckv_trim_graph_q8(const ckv_q8_desc* cache, const ckv_graph_desc* graph, ckv_stream_t stream);
 
 /*
  * Reads the graph's device error word (ckv_graph_desc.dev_err, an OR of
@@ -581,7 +611,8 @@ typedef enum {
     CKV_KERNEL_SELECT = 2,     /* no kernel (kept so the kinds keep their numbers) */
     CKV_KERNEL_ATTENTION = 3,  /* split-K attention (sparse and dense decode) */
     CKV_KERNEL_MERGE = 4,      /* merge, neighbours and fused update */
-    CKV_KERNEL_UPDATE = 5,     /* ckv_assign_update / ckv_append_assign; ckv_plan_blocks, ckv_quant_append, ckv_q8_read */
+    CKV_KERNEL_UPDATE = 5,     /* ckv_assign_update / ckv_append_assign; ckv_plan_blocks, ckv_quant_append, ckv_q8_read,
+                                  ckv_trim_graph_q8 */
     CKV_KERNEL_EDGES = 6       /* the four kernels of ckv_build_edges, as one */
 } ckv_kernel_kind;
 #define CKV_KERNEL_KINDS 7

@@ -1,0 +1,367 @@
+"""Community graphs over the paged 8-bit cache when its requests do not simply grow: growth refused after a token has
+joined, idle requests, tokens given back, requests that end.  A join that is undone leaves no trace, which is compared bit
+for bit with the state before it; no position is ever attended twice."""
+import ctypes
+import re
+
+import numpy as np
+import pytest
+import torch
+
+import graph_community_sparse_b200 as ckv
+from graph_community_sparse_b200.layer import PagedLayerState
+from test_abi import CAPACITY, FAKE, HEADER, INVALID, _graph
+from test_q8_abi import _q8, _table
+
+DEV = "cuda"
+R = ctypes.byref
+FIELDS = ("comm_of", "offs", "cnt", "cent", "cent_q", "cent_qs", "num_comm", "tail_len", "built")
+
+
+def i32(x):
+    return torch.tensor(list(x), dtype=torch.int32, device=DEV)
+
+
+# ---------------------------------------------------------------------------
+# without a GPU
+# ---------------------------------------------------------------------------
+
+TRIMS = [
+    ("cache", lambda: (_q8(d=96), _graph()), "unsupported"),
+    ("graph mode", lambda: (_q8(), _graph(mode=2, undo=FAKE, built=FAKE)), INVALID),
+    ("graph T_cap", lambda: (_q8(), _graph(T_cap=8192, undo=FAKE, built=FAKE)), CAPACITY),
+    ("no undo", lambda: (_q8(), _graph(built=FAKE)), INVALID),
+    ("no built", lambda: (_q8(), _graph(undo=FAKE)), INVALID),
+]
+
+
+@pytest.mark.parametrize("name,make,status", TRIMS, ids=[t[0] for t in TRIMS])
+def test_trim_refusals(name, make, status):
+    cache, graph = make()
+    got = ckv.lib.ckv_trim_graph_q8(R(cache), R(graph), None)
+    assert got == (3 if status == "unsupported" else status), ckv.ckv_last_error()
+    assert ckv.ckv_last_error()
+
+
+def test_trim_null_descriptors():
+    assert ckv.lib.ckv_trim_graph_q8(None, R(_graph()), None) == INVALID
+    assert ckv.lib.ckv_trim_graph_q8(R(_q8(_table())), None, None) == INVALID
+    src = open(HEADER).read()
+    assert int(re.search(r"#define CKV_DEVERR_CUT (\d+)", src).group(1)) == ckv.DEVERR_CUT
+
+
+def test_binding_refuses_another_cachess_graph():
+    a, b = (ckv.new_q8_cache(B, 2, 4, 64, 8, 16, 4, device="cpu") for B in (2, 3))
+    graph = ckv.new_graph(ckv.q8_shape(b, 64), ckv.PER_GROUP, 0, 4, 4, device="cpu", undo=True)
+    assert graph.undo.shape == (6, 4, 64) and graph.built.tolist() == [0] * 6
+    assert ckv.new_graph(ckv.q8_shape(b, 64), ckv.PER_GROUP, 0, 4, 4, device="cpu").undo is None
+    with pytest.raises(ValueError):
+        ckv.ckv_trim_graph_q8(a, graph)
+    with pytest.raises(ValueError):  # not on a GPU
+        ckv.ckv_trim_graph_q8(b, graph)
+
+
+# ---------------------------------------------------------------------------
+# on the GPU
+# ---------------------------------------------------------------------------
+
+class Batch:
+    """Requests of T tokens with communities, and decode steps over them."""
+
+    def __init__(self, B=3, mode="group", T=90, d=64, dtype=torch.float32, fmt="int8", S=4, C=5, max_tail=8, n_blocks=60,
+                 rule="score", seed=0):
+        self.gen = torch.Generator().manual_seed(seed)
+        self.Hkv, self.Hq, self.d, self.B, self.C, self.S = 2, 4, d, B, C, S
+        self.cache = ckv.new_q8_cache(B, 2, 4, d, n_blocks, 16, 12, fmt, dtype)
+        self.st = PagedLayerState(self.cache, mode, S, C, max_tail, T_cap=160, rule=rule)
+        self.G = 2 if mode == "group" else 4
+        self.mu = torch.randn((C, d), generator=self.gen)
+        lab = torch.randint(0, C, (B, 2, T), generator=self.gen)
+        K = self.mu[lab] + 0.3 * torch.randn((B, 2, T, d), generator=self.gen)
+        V = torch.randn((B, 2, T, d), generator=self.gen)
+        K, V = (x.to(dtype).to(DEV).transpose(1, 2) for x in (K, V))
+        self.st.grow(i32([T] * B), B * T)
+        self.st.write(K, V)
+        self.labels = lab[:, :, None, :].expand(B, 2, self.G // 2, T).reshape(B * self.G, T).to(torch.int32).clone()
+        self.labels[:, :S] = -1
+        self.st.build(self.labels.to(DEV), T)
+
+    def q(self):
+        return torch.randn((self.B, 4, self.d), generator=self.gen).to(self.cache.dtype).to(DEV)
+
+    def rows(self):
+        k = self.mu[torch.randint(0, self.C, (self.B, 2), generator=self.gen)] + 0.3 * torch.randn((self.B, 2, self.d), generator=self.gen)
+        v = torch.randn((self.B, 2, self.d), generator=self.gen)
+        return tuple(x.to(self.cache.dtype).to(DEV) for x in (k, v))
+
+    def join(self, k, q=None):
+        q = self.q() if q is None else q
+        self.st.select(q, 10 ** 6)
+        return self.st.attend(q, k).clone()
+
+    def step(self, add):
+        """Attend and join, then grow by `add`; rows for every token added."""
+        k, v = self.rows()
+        out = self.join(k)
+        p = self.st.grow(i32(add), self.B)
+        live = [b for b, a in enumerate(add) if a > 0]
+        pad = self.B - len(live)
+        packed = [torch.cat([x[live], torch.zeros((pad, 2, self.d), dtype=x.dtype, device=DEV)]) for x in (k, v)]
+        self.st.write(*packed)
+        return p, out
+
+    def state(self):
+        g = self.st.graph
+        s = {f: getattr(g, f).clone() for f in FIELDS}
+        for f in ("tail_tok", "tail_comm"):
+            s[f] = [getattr(g, f)[u, : int(g.tail_len[u])].tolist() for u in range(g.U)]
+        return s
+
+    def check_lists(self):
+        """Every token that a community holds is listed once when all communities are selected."""
+        self.st.select(self.q(), 10 ** 6)
+        g, sel = self.st.graph, self.st.sel
+        assert int(sel.n_sel.min()) >= 0
+        for u in range(g.U):
+            n = int(self.cache.len[u // self.G])
+            got = sel.sel_tok[u, : int(sel.n_tok[u])].tolist()
+            held = [t for t, c in enumerate(g.comm_of[u].tolist()) if c >= 0]
+            assert sorted(got) == sorted(list(range(self.S)) + held), u
+            assert len(set(got)) == len(got) and (not held or max(held) < n)
+            assert int(g.cnt[u].sum()) == len(held)
+
+    def errors(self):
+        return ckv.ckv_get_device_error(self.cache, reset=True), ckv.ckv_get_device_error(self.st.graph, reset=True)
+
+
+def same(a, b, rows=None):
+    for f in a:
+        x, y = a[f], b[f]
+        if rows is not None:
+            x, y = [x[u] for u in rows], [y[u] for u in rows]
+            assert all(torch.equal(p, q) if torch.is_tensor(p) else p == q for p, q in zip(x, y)), f
+        else:
+            assert torch.equal(x, y) if torch.is_tensor(x) else x == y, f
+
+
+KINDS = [dict(), dict(mode="head", d=128, dtype=torch.bfloat16), dict(fmt="e4m3", rule="vote"), dict(C=1, S=0, mode="head")]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", KINDS)
+def test_tokens_given_back_leave_their_communities(kw):
+    b = Batch(**kw)
+    b.step([1, 1, 1])
+    before, lens = b.state(), b.cache.len.tolist()
+    for _ in range(3):
+        p, _ = b.step([1, 1, 1])
+        assert p.granted.tolist() == [1, 1, 1]
+    middle = b.state()
+    assert b.st.graph.tail_len.tolist() == [4] * b.st.graph.U
+    # request 0 keeps all, 1 loses two, 2 loses the three
+    b.st.grow(i32([0, -2, -3]), 0)
+    after = b.state()
+    same(middle, after, range(b.G))
+    same(before, after, range(2 * b.G, 3 * b.G))
+    assert after["tail_len"].tolist() == [4] * b.G + [2] * b.G + [1] * b.G
+    b.check_lists()
+    # the same positions again, with other keys
+    for _ in range(3):
+        b.step([1, 1, 1])
+        b.check_lists()
+    assert b.cache.len.tolist() == [lens[0] + 6, lens[1] + 4, lens[2] + 3]
+    b.st.grow(i32([-6, -4, -3]), 0)
+    same(before, b.state())
+    assert b.errors() == (0, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", KINDS)
+def test_a_refused_or_idle_token_joins_nothing(kw):
+    """Room for request 0 alone; request 2 adds nothing; the retry joins the position once."""
+    T = 95
+    b = Batch(T=T, n_blocks=3 * 6 + 1, **kw)
+    b.step([1, 1, 0])  # 96 tokens: six whole blocks
+    before = b.state()
+    assert before["tail_len"].tolist() == [1] * b.G + [1] * b.G + [0] * b.G
+    p, _ = b.step([1, 1, 0])
+    assert p.granted.tolist() == [1, 0, 0]
+    assert b.errors() == (ckv.DEVERR_PLAN, 0)
+    same(before, b.state(), range(b.G, 3 * b.G))
+    b.check_lists()
+    b.st.grow(i32([-2, 0, 0]), 0)  # a block comes back
+    p, _ = b.step([0, 1, 1])
+    assert p.granted.tolist() == [0, 1, 1]
+    b.check_lists()
+    g = b.st.graph
+    assert g.tail_tok[b.G: 2 * b.G, :2].tolist() == [[T, T + 1]] * b.G
+    assert g.tail_tok[2 * b.G:, :1].tolist() == [[T]] * b.G
+    assert g.tail_len.tolist() == [0] * b.G + [2] * b.G + [1] * b.G
+    assert b.errors() == (0, 0)
+
+
+@pytest.mark.gpu
+def test_the_same_position_joined_again_replaces_the_first():
+    """Two joins with no growth between them leave what the second alone would."""
+    a, b = Batch(seed=5), Batch(seed=5)
+    q = a.q()
+    k1, k2 = a.rows()[0], a.rows()[0]
+    a.st.select(q, 10 ** 6)
+    a.st.attend(q, k1)
+    a.st.attend(q, k2)
+    b.st.select(q, 10 ** 6)
+    b.st.attend(q, k2)
+    same(a.state(), b.state())
+    assert torch.equal(a.st.assigned, b.st.assigned) and a.st.graph.tail_len.tolist() == [1] * a.st.graph.U
+    # a graph without room to undo does not join it a second time
+    shape, ws = a.st.shape, a.st.graph_ws
+    plain = ckv.new_graph(shape, ckv.PER_GROUP, a.S, a.C, 8)
+    k, _ = a.st.read(90)
+    rows = ckv.CacheDesc(shape.dtype, shape.B, shape.Hkv, shape.Hq, shape.d, shape.T_cap, k.data_ptr(), k.data_ptr(),
+                         k.stride(0), k.stride(1), k.stride(2))
+    ckv.ckv_build_centroids(rows, a.labels.to(DEV), 90, plain, ws)
+    ckv.ckv_score_select(shape, plain, q, 10 ** 6, a.st.sel, ws)
+    for i, key in enumerate((k1, k2)):
+        ckv.ckv_sparse_decode_q8(a.cache, q, plain, a.st.sel, a.st.out, None, a.st.ws, key, a.st.assigned)
+        assert (a.st.assigned >= 0).all() == (i == 0)
+        assert plain.tail_len.tolist() == [1] * plain.U
+    assert (a.st.assigned == -1).all() and int(plain.dev_err) == ckv.DEVERR_INDEX
+    with pytest.raises(ckv.CKVError):
+        ckv.ckv_trim_graph_q8(a.cache, plain)
+
+
+@pytest.mark.gpu
+def test_an_ended_request_loses_its_communities_and_no_other():
+    b = Batch()
+    b.step([1, 1, 1])
+    before = b.state()
+    b.st.grow(i32([0, -10 ** 6, 0]), 0)
+    after = b.state()
+    mine = range(b.G, 2 * b.G)
+    same(before, after, [u for u in range(3 * b.G) if u not in mine])
+    for u in mine:
+        assert not after["cnt"][u].any() and not after["offs"][u].any() and (after["comm_of"][u] == -1).all()
+        assert int(after["num_comm"][u]) == int(after["tail_len"][u]) == int(after["built"][u]) == 0
+    assert b.errors() == (0, 0)  # an end is no fault
+    b.st.select(b.q(), 10 ** 6)
+    assert [int(b.st.sel.n_tok[u]) for u in mine] == [b.S] * b.G and [int(b.st.sel.n_sel[u]) for u in mine] == [0] * b.G
+    # below the build's positions without an end: emptied, and said so
+    b.st.grow(i32([-30, 0, 0]), 0)
+    assert b.errors() == (0, ckv.DEVERR_CUT)
+    same(before, b.state(), range(2 * b.G, 3 * b.G))
+    assert int(b.st.graph.num_comm[: 2 * b.G].max()) == 0
+
+
+@pytest.mark.gpu
+def test_a_join_below_the_builds_positions_is_refused():
+    """Lengths set behind the plan's back: the position is a member already."""
+    b = Batch()
+    before = b.state()
+    b.cache.len[1] = 50
+    b.join(b.rows()[0])
+    after = b.state()
+    same(before, after, range(b.G, 2 * b.G))
+    assert b.st.assigned[b.G: 2 * b.G].tolist() == [-1] * b.G and int(b.st.assigned[: b.G].min()) >= 0
+    assert b.errors()[1] == ckv.DEVERR_CUT
+    b.cache.len[1] = 10 ** 6  # a bad length: nothing is done for this request
+    b.cache.len[2] = -1
+    ckv.ckv_trim_graph_q8(b.cache, b.st.graph)
+    assert b.errors()[0] == ckv.DEVERR_BLOCK
+    same(after, b.state(), range(b.G, 3 * b.G))
+
+
+@pytest.mark.gpu
+def test_full_tails_and_long_drops():
+    """More joins than the tail holds, then all of them given back."""
+    b = Batch(max_tail=3)
+    before = b.state()
+    for _ in range(5):
+        b.step([1, 1, 1])
+    assert b.st.graph.tail_len.tolist() == [3] * b.st.graph.U
+    assert b.errors() == (0, ckv.DEVERR_TAIL_FULL)
+    b.check_lists()
+    b.st.grow(i32([-1, -3, -5]), 0)
+    assert b.st.graph.tail_len.tolist() == [3] * b.G + [2] * b.G + [0] * b.G
+    same(before, b.state(), range(2 * b.G, 3 * b.G))
+    none = Batch(max_tail=0)
+    before = none.state()
+    none.step([1, 1, 1])
+    none.st.grow(i32([-1, 0, 0]), 0)
+    same(before, none.state())
+    assert none.errors() == (0, ckv.DEVERR_TAIL_FULL)
+
+
+@pytest.mark.gpu
+def test_captured_steps_with_drops():
+    """Two steps and a drop of one token, captured and replayed, against the same calls made eagerly."""
+    a, b = Batch(seed=3), Batch(seed=3)
+    q, (k, v) = a.q(), a.rows()
+    one, back = i32([1, 1, 1]), i32([-1, 0, -1])
+
+    def work(x):
+        for add in (one, one):
+            x.st.select(q, 60)
+            x.st.attend(q, k)
+            x.st.grow(add, 3)
+            x.st.write(k, v)
+        x.st.grow(back, 0)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work(b)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        work(b)
+    work(a)
+    for _ in range(2):
+        work(a)
+        g.replay()
+        torch.cuda.synchronize()
+        same(a.state(), b.state())
+        assert torch.equal(a.st.out, b.st.out) and a.cache.len.tolist() == b.cache.len.tolist()
+    b.check_lists()
+    assert b.errors() == (0, 0)
+
+
+@pytest.mark.gpu
+def test_the_debug_build_trims_alike():
+    b = Batch()
+    before = b.state()
+    b.step([1, 1, 1])
+    b.cache.len.sub_(1)
+    dbg = ckv.load_debug_library()
+    assert dbg.ckv_trim_graph_q8(R(b.cache.desc), R(b.st.graph.desc), torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    same(before, b.state())
+
+
+@pytest.mark.gpu
+def test_restored_centres_are_the_oracles():
+    """After a drop the centres are the plain running means of what is left: the labelled values and the joined keys."""
+    b = Batch(dtype=torch.float32)
+    g = b.st.graph
+    held, _ = b.st.read(90)
+    joined = [{} for _ in range(g.U)]
+    for i in range(4):
+        k, v = b.rows()
+        b.join(k)
+        for u in range(g.U):
+            joined[u][90 + i] = (int(b.st.assigned[u]), k[u // b.G, u % b.G].double().cpu().numpy())
+        b.st.grow(i32([1, 1, 1]), 3)
+        b.st.write(k, v)
+    b.st.grow(i32([-1, -2, -3]), 0)
+    for u in range(g.U):
+        req, kv = u // b.G, u % b.G
+        n = int(b.cache.len[req])
+        keys = held[req, kv].double().cpu().numpy()
+        for c in range(b.C):
+            rows = [keys[t] for t in range(b.S, 90) if int(b.labels[u, t]) == c]
+            rows += [x for t, (cc, x) in joined[u].items() if cc == c and t < n]
+            assert int(g.cnt[u, c]) == len(rows)
+            if rows:
+                # the mean's own rounding, and at most four steps of it with three each (k - c, times 1/(n + 1), n >= 1;
+                # plus c), each at most 2^-24 of the largest value: 13 of them
+                err = np.abs(g.cent[u, c].double().cpu().numpy() - np.mean(rows, 0)).max()
+                assert err <= 13 * 2.0 ** -24 * np.abs(rows).max()
