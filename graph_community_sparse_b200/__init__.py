@@ -32,7 +32,8 @@ __all__ = [
     "NEIGHBOURS",
     "Q8_INT8", "Q8_E4M3", "DEVERR_PLAN", "DEVERR_BLOCK", "DEVERR_CUT", "TableDesc", "Q8Desc", "PlanDesc", "BlockTable", "Q8Cache",
     "Plan", "block_table", "q8_cache", "new_q8_cache", "new_plan", "q8_shape", "ckv_plan_blocks", "ckv_quant_append",
-    "ckv_q8_read", "ckv_q8_workspace_size", "ckv_dense_decode_q8", "ckv_sparse_decode_q8", "ckv_trim_graph_q8",
+    "ckv_q8_read", "ckv_q8_workspace_size", "ckv_dense_decode_q8", "ckv_sparse_decode_q8", "ckv_build_centroids_q8",
+    "ckv_trim_graph_q8",
 ]
 
 # the in-tree build, always: no environment variable selects another library
@@ -56,7 +57,7 @@ EXPORTED = ("ckv_workspace_size", "ckv_build_centroids", "ckv_score_select", "ck
             "ckv_dense_decode",
             "ckv_edges_workspace_size", "ckv_build_edges",
             "ckv_plan_blocks", "ckv_quant_append", "ckv_q8_read", "ckv_q8_workspace_size", "ckv_dense_decode_q8",
-            "ckv_sparse_decode_q8", "ckv_trim_graph_q8",
+            "ckv_sparse_decode_q8", "ckv_build_centroids_q8", "ckv_trim_graph_q8",
             "ckv_status_string", "ckv_last_error", "ckv_abi_version", "ckv_debug_build")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -131,6 +132,7 @@ def _declare(lib_: ctypes.CDLL) -> ctypes.CDLL:
     lib_.ckv_dense_decode_q8.argtypes = [_P(Q8Desc), _p, _p, _p, _sz, _p]
     lib_.ckv_sparse_decode_q8.argtypes = [_P(Q8Desc), _p, _P(GraphDesc), _P(SelectionDesc), _p, _p, _p, _p, _p, _sz,
                                           _p]
+    lib_.ckv_build_centroids_q8.argtypes = [_P(Q8Desc), _p, _i64, _i32, _p, _P(GraphDesc), _p, _sz, _p]
     lib_.ckv_trim_graph_q8.argtypes = [_P(Q8Desc), _P(GraphDesc), _p]
     lib_.ckv_get_device_error.argtypes = [_P(GraphDesc), _p, _P(ctypes.c_int32), _i32]
     lib_.ckv_kernel_timing.argtypes = [_i32]
@@ -139,7 +141,8 @@ def _declare(lib_: ctypes.CDLL) -> ctypes.CDLL:
               "ckv_sparse_decode_noalloc", "ckv_assign_update", "ckv_append_assign", "ckv_sparse_decode_append",
               "ckv_dense_decode", "ckv_get_device_error", "ckv_kernel_timing", "ckv_kernel_times",
               "ckv_edges_workspace_size", "ckv_build_edges", "ckv_plan_blocks", "ckv_quant_append", "ckv_q8_read",
-              "ckv_q8_workspace_size", "ckv_dense_decode_q8", "ckv_sparse_decode_q8", "ckv_trim_graph_q8"):
+              "ckv_q8_workspace_size", "ckv_dense_decode_q8", "ckv_sparse_decode_q8", "ckv_build_centroids_q8",
+              "ckv_trim_graph_q8"):
         getattr(lib_, f).restype = ctypes.c_int
     lib_.ckv_status_string.argtypes = [ctypes.c_int]
     lib_.ckv_status_string.restype = ctypes.c_char_p
@@ -757,11 +760,30 @@ def ckv_sparse_decode_q8(cache: Q8Cache, q: torch.Tensor, graph: Graph, sel: Sel
           ctypes.byref(sel.desc), op, np_, kp, ap, ws.data_ptr(), ws.numel())
 
 
+def _of_graph(cache: Q8Cache, graph: Graph) -> None:
+    U = cache.B * (cache.Hq if graph.desc.mode == PER_HEAD else cache.Hkv)
+    if graph.U != U or graph.dev_err.device != cache.device:
+        raise ValueError("the graph must be for this cache's batch and heads, on its device")
+
+
+def ckv_build_centroids_q8(cache: Q8Cache, labels: torch.Tensor, T: int, graph: Graph, ws: torch.Tensor,
+                           which: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Community state from labels (int32 [U, >= T], T at least the longest request) over each request's own positions
+    [0, len[b]); which (int32 [B]): only the requests that are not 0 there."""
+    _of_graph(cache, graph)
+    dev = cache.device
+    if (labels.dtype is not torch.int32 or labels.dim() != 2 or labels.shape[0] != graph.U or labels.shape[1] < T
+            or labels.stride(1) != 1 or labels.device != dev):
+        raise ValueError(f"labels must be int32 [{graph.U}, >= {T}] on {dev} with contiguous rows")
+    if ws.device != dev:
+        raise ValueError("the workspace is on another device")
+    wp = None if which is None else _need("which", which, torch.int32, cache.blocks.shape, dev)
+    _call("ckv_build_centroids_q8", lib.ckv_build_centroids_q8, dev, stream, cache.ref, labels.data_ptr(),
+          labels.stride(0) if graph.U > 1 else labels.shape[1], T, wp, ctypes.byref(graph.desc), ws.data_ptr(), ws.numel())
+
+
 def ckv_trim_graph_q8(cache: Q8Cache, graph: Graph, stream=None) -> None:
     """Takes the tokens at or past each request's length out of its communities: after a ckv_plan_blocks that may have
     refused a joined token or dropped tokens, before the next ckv_score_select.  The graph needs new_graph(undo=True)."""
-    dev = cache.device
-    U = cache.B * (cache.Hq if graph.desc.mode == PER_HEAD else cache.Hkv)
-    if graph.U != U or graph.dev_err.device != dev:
-        raise ValueError("the graph must be for this cache's batch and heads, on its device")
-    _call("ckv_trim_graph_q8", lib.ckv_trim_graph_q8, dev, stream, cache.ref, ctypes.byref(graph.desc))
+    _of_graph(cache, graph)
+    _call("ckv_trim_graph_q8", lib.ckv_trim_graph_q8, cache.device, stream, cache.ref, ctypes.byref(graph.desc))

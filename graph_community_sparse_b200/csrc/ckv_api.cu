@@ -620,6 +620,24 @@ ckv_status ckv_sparse_decode_q8(const ckv_q8_desc* cache, const void* q, const c
                        "ckv_sparse_decode_q8");
 }
 
+ckv_status ckv_build_centroids_q8(const ckv_q8_desc* cache, const int32_t* labels, int64_t labels_stride, int32_t T,
+                                  const int32_t* which, const ckv_graph_desc* graph, void* ws, size_t ws_bytes,
+                                  ckv_stream_t stream) {
+    CKV_TRY(check_q8(cache));
+    CKV_TRY(check_q8_graph(cache, graph));
+    if (!labels) return fail(CKV_ERR_INVALID_ARG, "labels is NULL");
+    if (T < graph->S) return fail(CKV_ERR_INVALID_ARG, "T = %d < S = %d", T, graph->S);
+    if (T > graph->T_cap) return fail(CKV_ERR_CAPACITY, "T = %d > T_cap = %d", T, graph->T_cap);
+    if (labels_stride < T) return fail(CKV_ERR_INVALID_ARG, "labels_stride < T");
+    const ckv_cache_desc shape = q8_shape(cache, graph->T_cap);
+    const int U = shape.B * graphs_per_seq(&shape, graph);
+    const size_t head = ckv::ws_head_bytes(shape.B, shape.Hq);
+    CKV_TRY(check_ws(ws, ws_bytes, head + ckv::build_ws_bytes(U, graph->Cmax, graph->T_cap)));
+    return cuda_status(ckv::launch_build_q8(q8_view(cache), graph_view(&shape, graph), labels, labels_stride, T, which,
+                                            static_cast<char*>(ws) + head, reinterpret_cast<cudaStream_t>(stream)),
+                       "ckv_build_centroids_q8");
+}
+
 ckv_status ckv_trim_graph_q8(const ckv_q8_desc* cache, const ckv_graph_desc* graph, ckv_stream_t stream) {
     CKV_TRY(check_q8(cache));
     CKV_TRY(check_q8_graph(cache, graph));

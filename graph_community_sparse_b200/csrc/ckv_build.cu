@@ -17,7 +17,11 @@
 //   fixed interleaving in fp64 and combine in warp order: deterministic, and
 //   the fp32 centre is the correctly rounded mean up to fp64 summation error;
 //   the row's int8 scoring copy (scale and codes) is written with it.
-#include "ckv_internal.cuh"
+//
+// Over a paged 8-bit cache (Q8) every request has its own number of positions,
+// those of its length, some requests may be left out, and a member's row is read
+// where it lies in the pool.
+#include "ckv_q8.cuh"
 
 namespace ckv {
 
@@ -39,18 +43,45 @@ struct BuildParams {
     int32_t* tail_len;
     int32_t* dev_err;
     int32_t* built;  // may be NULL
+    // Q8
+    TableView t;
+    const float* k_scale;
+    const int32_t* which;  // requests to build, NULL: all
 };
 
+// Positions of unit u that take part; -1: its request is left alone.
+template <bool Q8>
+__device__ __forceinline__ int build_len(const BuildParams& p, int u) {
+    if constexpr (Q8) {
+        const int b = u / p.G;
+        if (p.which && p.which[b] == 0) return -1;
+        const int n = p.t.len[b];
+        return n < 0 || n > (long long)p.t.max_blocks << p.t.sh ? 0 : min(n, p.T);
+    } else {
+        return p.T;
+    }
+}
+
+template <bool Q8>
 __global__ void __launch_bounds__(256) build_hist(BuildParams p) {
     extern __shared__ int hist[];
     const int u = blockIdx.y, chunk = blockIdx.x;
+    const int T = build_len<Q8>(p, u);
+    if (T < 0) return;
+    if constexpr (Q8) {
+        if (chunk == 0 && threadIdx.x == 0) {
+            const int n = p.t.len[u / p.G];
+            if (n < 0 || n > (long long)p.t.max_blocks << p.t.sh) atomicOr(p.t.dev_err, CKV_DEVERR_BLOCK);
+            else if (n > p.T) atomicOr(p.dev_err, CKV_DEVERR_LABEL_RANGE);  // tokens without a label
+        }
+    }
     for (int c = threadIdx.x; c < p.Cmax; c += blockDim.x) hist[c] = 0;
     __syncthreads();
     const int t0 = chunk * BUILD_CHUNK, t1 = min(t0 + BUILD_CHUNK, p.T_cap);
     int err = 0;
     for (int t = t0 + threadIdx.x; t < t1; t += blockDim.x) {
         int lab = -1;
-        if (t < p.T) {
+        if (t < T) {
             lab = p.labels[(size_t)u * p.lstride + t];
             if (t < p.S) {
                 if (lab != -1) err |= CKV_DEVERR_SINK_LABEL;
@@ -70,10 +101,13 @@ __global__ void __launch_bounds__(256) build_hist(BuildParams p) {
     for (int c = threadIdx.x; c < p.Cmax; c += blockDim.x) dst[c] = hist[c];
 }
 
+template <bool Q8>
 __global__ void __launch_bounds__(1024) build_scan(BuildParams p) {
     __shared__ int s_warp[33];
     __shared__ int s_maxc;
     const int u = blockIdx.x;
+    const int T = build_len<Q8>(p, u);
+    if (T < 0) return;
     if (threadIdx.x == 0) s_maxc = -1;
     __syncthreads();
     int32_t* base = p.counts + (size_t)u * p.nchunks * p.Cmax;
@@ -103,17 +137,20 @@ __global__ void __launch_bounds__(1024) build_scan(BuildParams p) {
         p.offs[(size_t)u * (p.Cmax + 1) + p.Cmax] = carry;
         p.num_comm[u] = s_maxc + 1;
         p.tail_len[u] = 0;
-        if (p.built) p.built[u] = p.T;
+        if (p.built) p.built[u] = T;
     }
 }
 
+template <bool Q8>
 __global__ void __launch_bounds__(32) build_scatter(BuildParams p) {
     extern __shared__ int cur[];
     const int u = blockIdx.y, chunk = blockIdx.x, lane = threadIdx.x;
+    const int T = build_len<Q8>(p, u);
+    if (T < 0) return;
     const int32_t* src = p.counts + ((size_t)u * p.nchunks + chunk) * p.Cmax;
     for (int c = lane; c < p.Cmax; c += 32) cur[c] = src[c];
     __syncwarp();
-    const int t0 = chunk * BUILD_CHUNK, t1 = min(t0 + BUILD_CHUNK, p.T);
+    const int t0 = chunk * BUILD_CHUNK, t1 = min(t0 + BUILD_CHUNK, T);
     const unsigned lt = (1u << lane) - 1u;
     for (int tb = t0; tb < t1; tb += 32) {
         const int t = tb + lane;
@@ -129,17 +166,80 @@ __global__ void __launch_bounds__(32) build_scatter(BuildParams p) {
     }
 }
 
+// Member rows: position t's elements lane E .. lane E + E - 1.  load() only loads, value()
+// converts, so that several rows are in flight.
 template <typename T, int D>
+struct RowsOfCache {
+    static constexpr int E = D / 32;
+    struct Raw {
+        T x[E];
+    };
+    const T* k;
+    int64_t st;
+    __device__ RowsOfCache(const BuildParams& p, int b, int kvh, int lane)
+        : k(static_cast<const T*>(p.k) + b * p.sb + kvh * p.sh + lane * E), st(p.st) {}
+    __device__ __forceinline__ Raw load(int t) const {
+        Raw r;
+#pragma unroll
+        for (int e = 0; e < E; ++e) r.x[e] = k[(int64_t)t * st + e];
+        return r;
+    }
+    __device__ __forceinline__ void value(const Raw& r, float (&x)[E]) const {
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = to_f32(r.x[e]);
+    }
+};
+
+// The values held, code * scale in fp32; zeros in a block out of range.
+template <int FMT, int D>
+struct RowsOfPool {
+    static constexpr int E = D / 32;
+    struct Raw {
+        unsigned codes;
+        float scale;
+    };
+    const TableView& t;
+    const int32_t* table;
+    const unsigned char* k;
+    const float* scale;
+    int Hkv, kvh;
+    __device__ RowsOfPool(const BuildParams& p, int b, int kvh, int lane)
+        : t(p.t), table(p.t.table + (size_t)b * p.t.max_blocks), k(static_cast<const unsigned char*>(p.k) + lane * E),
+          scale(p.k_scale), Hkv(p.Hkv), kvh(kvh) {}
+    __device__ __forceinline__ Raw load(int pos) const {
+        const int id = table[pos >> t.sh];
+        Raw r{0u, 0.f};
+        if ((unsigned)id >= (unsigned)t.n_blocks) {
+            atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
+            return r;
+        }
+        const size_t unit = (size_t)id * Hkv + kvh;
+        const unsigned char* row = k + ((unit << t.sh) + (pos & (t.block - 1))) * D;
+        if constexpr (E == 4) r.codes = *reinterpret_cast<const unsigned*>(row);
+        else r.codes = *reinterpret_cast<const unsigned short*>(row);
+        r.scale = scale[unit];
+        return r;
+    }
+    __device__ __forceinline__ void value(const Raw& r, float (&x)[E]) const {
+        float y[4];
+        q8c_values<FMT>(r.codes, y);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = y[e] * r.scale;
+    }
+};
+
+template <typename Rows, int D, bool Q8>
 __global__ void __launch_bounds__(256) build_mean(BuildParams p) {
     constexpr int E = D / 32;
     __shared__ double part[8][D];
     const int c = blockIdx.x, u = blockIdx.y;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (Q8 && build_len<Q8>(p, u) < 0) return;
     const int b = u / p.G, g = u - b * p.G;
     const int kvh = p.per_head ? g / (p.Hq / p.Hkv) : g;
     const int beg = p.offs[(size_t)u * (p.Cmax + 1) + c];
     const int n = p.offs[(size_t)u * (p.Cmax + 1) + c + 1] - beg;
-    const T* Kb = static_cast<const T*>(p.k) + b * p.sb + kvh * p.sh + lane * E;
+    const Rows rows(p, b, kvh, lane);
     const int32_t* tk = p.tok + (size_t)u * p.T_cap + beg;
     double acc[E];
 #pragma unroll
@@ -149,20 +249,22 @@ __global__ void __launch_bounds__(256) build_mean(BuildParams p) {
         int t[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) t[r] = tk[i + 8 * r];
-        T x[4][E];
+        typename Rows::Raw raw[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 4; ++r) raw[r] = rows.load(t[r]);
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[r][e] = Kb[(int64_t)t[r] * p.st + e];
+        for (int r = 0; r < 4; ++r) {
+            float x[E];
+            rows.value(raw[r], x);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] += (double)to_f32(x[r][e]);
+            for (int e = 0; e < E; ++e) acc[e] += (double)x[e];
+        }
     }
     for (; i < n; i += 8) {
-        const int t = tk[i];
+        float x[E];
+        rows.value(rows.load(tk[i]), x);
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += (double)to_f32(Kb[(int64_t)t * p.st + e]);
+        for (int e = 0; e < E; ++e) acc[e] += (double)x[e];
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
@@ -195,13 +297,10 @@ size_t build_ws_bytes(int U, int Cmax, int T_cap) {
     return align256((size_t)U * nchunks * Cmax * 4);
 }
 
-cudaError_t launch_build(const CacheView& c, const GraphView& g, const int32_t* labels,
-                         int64_t labels_stride, int T, void* ws, cudaStream_t st) {
+// The fields that come from the graph and the labels.
+static BuildParams build_params(const GraphView& g, const int32_t* labels, int64_t labels_stride, int T, int Hq, int Hkv,
+                                void* ws) {
     BuildParams p{};
-    p.k = c.k;
-    p.sb = c.sb;
-    p.sh = c.sh;
-    p.st = c.st;
     p.labels = labels;
     p.lstride = labels_stride;
     p.T = T;
@@ -209,8 +308,8 @@ cudaError_t launch_build(const CacheView& c, const GraphView& g, const int32_t* 
     p.S = g.S;
     p.Cmax = g.Cmax;
     p.G = g.G;
-    p.Hq = c.Hq;
-    p.Hkv = c.Hkv;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
     p.per_head = g.mode == CKV_GRAPH_PER_HEAD;
     p.nchunks = (g.T_cap + BUILD_CHUNK - 1) / BUILD_CHUNK;
     p.counts = static_cast<int32_t*>(ws);
@@ -225,29 +324,57 @@ cudaError_t launch_build(const CacheView& c, const GraphView& g, const int32_t* 
     p.tail_len = g.tail_len;
     p.dev_err = g.dev_err;
     p.built = g.built;
-    const int U = c.B * g.G;
-    const size_t hsm = (size_t)g.Cmax * 4;
+    return p;
+}
+
+template <bool Q8>
+static cudaError_t launch_build_t(const BuildParams& p, int U, void (*mean)(BuildParams), cudaStream_t st) {
+    const size_t hsm = (size_t)p.Cmax * 4;
     static LaunchCache lc_hist, lc_scatter;
-    cudaError_t e = prepare_launch(build_hist, lc_hist, hsm, 256, nullptr, nullptr);
+    cudaError_t e = prepare_launch(build_hist<Q8>, lc_hist, hsm, 256, nullptr, nullptr);
     if (e != cudaSuccess) return e;
-    e = prepare_launch(build_scatter, lc_scatter, hsm, 32, nullptr, nullptr);
+    e = prepare_launch(build_scatter<Q8>, lc_scatter, hsm, 32, nullptr, nullptr);
     if (e != cudaSuccess) return e;
     const bool timed = timing_enabled();  // the four build kernels as one
     if (timed && (e = timing_mark(KK_BUILD, true, st)) != cudaSuccess) return e;
-    build_hist<<<dim3(p.nchunks, U), 256, hsm, st>>>(p);
-    build_scan<<<U, 1024, 0, st>>>(p);
-    build_scatter<<<dim3(p.nchunks, U), 32, hsm, st>>>(p);
-    const dim3 mg(g.Cmax, U);
-    if (c.dtype == CKV_DTYPE_BF16) {
-        if (c.d == 128) build_mean<__nv_bfloat16, 128><<<mg, 256, 0, st>>>(p);
-        else build_mean<__nv_bfloat16, 64><<<mg, 256, 0, st>>>(p);
-    } else {
-        if (c.d == 128) build_mean<float, 128><<<mg, 256, 0, st>>>(p);
-        else build_mean<float, 64><<<mg, 256, 0, st>>>(p);
-    }
+    build_hist<Q8><<<dim3(p.nchunks, U), 256, hsm, st>>>(p);
+    build_scan<Q8><<<U, 1024, 0, st>>>(p);
+    build_scatter<Q8><<<dim3(p.nchunks, U), 32, hsm, st>>>(p);
+    mean<<<dim3(p.Cmax, U), 256, 0, st>>>(p);
     e = cudaGetLastError();
     if (timed && e == cudaSuccess) e = timing_mark(KK_BUILD, false, st);
     return e;
+}
+
+cudaError_t launch_build(const CacheView& c, const GraphView& g, const int32_t* labels,
+                         int64_t labels_stride, int T, void* ws, cudaStream_t st) {
+    BuildParams p = build_params(g, labels, labels_stride, T, c.Hq, c.Hkv, ws);
+    p.k = c.k;
+    p.sb = c.sb;
+    p.sh = c.sh;
+    p.st = c.st;
+    const bool wide = c.d == 128;
+    const auto mean = c.dtype == CKV_DTYPE_BF16
+                          ? (wide ? build_mean<RowsOfCache<__nv_bfloat16, 128>, 128, false>
+                                  : build_mean<RowsOfCache<__nv_bfloat16, 64>, 64, false>)
+                          : (wide ? build_mean<RowsOfCache<float, 128>, 128, false>
+                                  : build_mean<RowsOfCache<float, 64>, 64, false>);
+    return launch_build_t<false>(p, c.B * g.G, mean, st);
+}
+
+cudaError_t launch_build_q8(const Q8View& c, const GraphView& g, const int32_t* labels, int64_t labels_stride, int T,
+                            const int32_t* which, void* ws, cudaStream_t st) {
+    BuildParams p = build_params(g, labels, labels_stride, T, c.Hq, c.Hkv, ws);
+    p.k = c.k;
+    p.t = c.t;
+    p.k_scale = c.k_scale;
+    p.which = which;
+    const bool wide = c.d == 128;
+    const auto mean = c.format == Q8_I8 ? (wide ? build_mean<RowsOfPool<Q8_I8, 128>, 128, true>
+                                                : build_mean<RowsOfPool<Q8_I8, 64>, 64, true>)
+                                        : (wide ? build_mean<RowsOfPool<Q8_E4, 128>, 128, true>
+                                                : build_mean<RowsOfPool<Q8_E4, 64>, 64, true>);
+    return launch_build_t<true>(p, c.t.B * g.G, mean, st);
 }
 
 }  // namespace ckv

@@ -1,5 +1,6 @@
 // The paged 8-bit cache: launch parameter packs and the code formats, shared by
-// its kernels (ckv_q8_cache.cu, ckv_q8_dense.cu, ckv_q8_sparse.cu).
+// its kernels (ckv_q8_cache.cu, ckv_q8_dense.cu, ckv_q8_sparse.cu) and the build
+// (ckv_build.cu).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -52,6 +53,8 @@ size_t q8_blocks_ws_bytes(int gq, int d);
 cudaError_t launch_dense_decode_q8(const Q8View& c, const void* q, float* out, void* ws, cudaStream_t st);
 cudaError_t launch_sparse_decode_q8(const Q8View& c, const GraphView& g, const SelView& s, const void* q, float* out,
                                     int32_t* nbr8, const void* k_new, int32_t* assigned, void* ws, cudaStream_t st);
+cudaError_t launch_build_q8(const Q8View& c, const GraphView& g, const int32_t* labels, int64_t labels_stride, int T,
+                            const int32_t* which, void* ws, cudaStream_t st);
 cudaError_t launch_trim_graph_q8(const Q8View& c, const GraphView& g, cudaStream_t st);
 
 // ---------------------------------------------------------------------------

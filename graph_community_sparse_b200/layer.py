@@ -16,7 +16,7 @@ from . import (ASSIGN_SCORE, ASSIGN_VOTE, PER_GROUP, PER_HEAD, Graph, Selection,
                ckv_sparse_decode_append,
                ckv_build_centroids, ckv_dense_decode, ckv_score_select, ckv_sparse_decode,
                ckv_workspace_size, new_graph, new_selection, new_workspace, NEIGHBOURS,
-               CacheDesc, Plan, Q8Cache, ckv_dense_decode_q8, ckv_plan_blocks, ckv_q8_read, ckv_q8_workspace_size,
+               CacheDesc, Plan, Q8Cache, ckv_build_centroids_q8, ckv_dense_decode_q8, ckv_plan_blocks, ckv_q8_read, ckv_q8_workspace_size,
                ckv_quant_append, ckv_sparse_decode_q8, ckv_trim_graph_q8, new_plan, q8_shape)
 
 
@@ -212,15 +212,15 @@ class PagedLayerState:
             ckv_dense_decode_q8(self.cache, q, out, self.ws, stream)
         return out
 
-    def build(self, labels: torch.Tensor, T: int, stream=None) -> None:
-        """Community state from labels (int32 [U, >= T]) over positions [0, T),
-        which every request must hold; the centres are those of the values held."""
-        k, v = self.read(T, stream=stream)
-        s = self.shape
-        rows = CacheDesc(s.dtype, s.B, s.Hkv, s.Hq, s.d, s.T_cap, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
-                         k.stride(2))
-        with _range("ckv_build_centroids"):
-            ckv_build_centroids(rows, labels, T, self.graph, self.graph_ws, stream)
+    def build(self, labels: torch.Tensor, T: Optional[int] = None, requests: Optional[torch.Tensor] = None,
+              stream=None) -> None:
+        """Community state from labels (int32 [U, >= T], T at least the longest
+        request) over each request's own positions; the centres are those of the
+        values held.  requests (int32 [B] on the device): only those that are not 0
+        there, e.g. a new one in the row of one that ended."""
+        with _range("ckv_build_centroids_q8"):
+            ckv_build_centroids_q8(self.cache, labels, labels.shape[1] if T is None else T, self.graph, self.graph_ws,
+                                   requests, stream)
 
     def select(self, q: torch.Tensor, budget: int, stream=None) -> None:
         with _range("ckv_score_select"):

@@ -515,8 +515,8 @@ CKV_API ckv_status ckv_quant_append(const ckv_q8_desc* cache, const ckv_plan_des
 
 /*
  * Reads rows of the 8-bit cache back in the cache's dtype (code * scale rounded
- * once): for ckv_build_centroids and ckv_build_edges, which take 16/32-bit
- * rows, or a prefill attention over what is cached.  Row r (0 <= r < R) of
+ * once): for ckv_build_edges, which takes 16-bit rows, or a prefill attention over
+ * what is cached.  Row r (0 <= r < R) of
  * request b, head h is position first[b] + r (first NULL: 0) and goes to
  * k_out + b * stride_b + h * stride_h + r * stride_t; positions outside
  * [0, len[b]) give zeros.  16-byte aligned rows; strides in elements; R <= 2^30,
@@ -570,6 +570,24 @@ CKV_API ckv_status ckv_sparse_decode_q8(const ckv_q8_desc* cache, const void* q,
                                         int32_t* assigned, void* ws, size_t ws_bytes, ckv_stream_t stream);
 
 /*
+ * ckv_build_centroids over the 8-bit cache: request b is built over its own
+ * positions [0, len[b]), its members' rows read in place from the pool (their values,
+ * code * scale in fp32).
+ *   labels  row u at labels + u * labels_stride, T entries, of which the first
+ *           len[b] count; T at least the longest request: where len[b] > T the
+ *           tokens from T on join no community (CKV_DEVERR_LABEL_RANGE).
+ *   which   int32 [B] or NULL: only requests with which[b] != 0 are built, the
+ *           graphs of the others stay as they are (a new request in the row of one
+ *           that ended).
+ * S <= T <= graph->T_cap.  A bad length counts as 0 and a block out of range as rows
+ * of zeros (CKV_DEVERR_BLOCK).  Workspace: ckv_workspace_size() for the cache's
+ * shapes (k = v = NULL, the graph's T_cap).
+ */
+CKV_API ckv_status ckv_build_centroids_q8(const ckv_q8_desc* cache, const int32_t* labels, int64_t labels_stride,
+                                          int32_t T, const int32_t* which, const ckv_graph_desc* graph, void* ws,
+                                          size_t ws_bytes, ckv_stream_t stream);
+
+/*
  * Brings a graph in step with the lengths that ckv_plan_blocks left: call it
  * after a ckv_plan_blocks that may refuse a joined token or drop tokens, before the
  * next ckv_score_select.  In every graph unit of request b the tail members at
@@ -606,7 +624,7 @@ CKV_API ckv_status ckv_get_device_error(const ckv_graph_desc* graph, ckv_stream_
  * arrays: CKV_ERR_INVALID_ARG; a failed event call: CKV_ERR_CUDA.
  */
 typedef enum {
-    CKV_KERNEL_BUILD = 0,      /* the four kernels of ckv_build_centroids, as one */
+    CKV_KERNEL_BUILD = 0,      /* the four kernels of ckv_build_centroids[_q8], as one */
     CKV_KERNEL_SCORE = 1,      /* ckv_score_select: scoring, selection and token list, one kernel */
     CKV_KERNEL_SELECT = 2,     /* no kernel (kept so the kinds keep their numbers) */
     CKV_KERNEL_ATTENTION = 3,  /* split-K attention (sparse and dense decode) */

@@ -1,5 +1,5 @@
-"""Community graphs over the paged 8-bit cache when its requests do not simply grow: growth refused after a token has
-joined, idle requests, tokens given back, requests that end.  A join that is undone leaves no trace, which is compared bit
+"""Community graphs over the paged 8-bit cache when its requests do not all start alike and simply grow: growth refused
+after a token has joined, idle requests, tokens given back, requests that end, requests of different length and new ones.  A join that is undone leaves no trace, which is compared bit
 for bit with the state before it; no position is ever attended twice."""
 import ctypes
 import re
@@ -10,7 +10,7 @@ import torch
 
 import graph_community_sparse_b200 as ckv
 from graph_community_sparse_b200.layer import PagedLayerState
-from test_abi import CAPACITY, FAKE, HEADER, INVALID, _graph
+from test_abi import CAPACITY, FAKE, HEADER, INVALID, WORKSPACE, _graph
 from test_q8_abi import _q8, _table
 
 DEV = "cuda"
@@ -41,6 +41,46 @@ def test_trim_refusals(name, make, status):
     got = ckv.lib.ckv_trim_graph_q8(R(cache), R(graph), None)
     assert got == (3 if status == "unsupported" else status), ckv.ckv_last_error()
     assert ckv.ckv_last_error()
+
+
+def _build(cache=None, graph=None, labels=FAKE, stride=4096, T=4096, ws=FAKE, n=1 << 40):
+    return ckv.lib.ckv_build_centroids_q8(R(cache or _q8()), labels, stride, T, None, R(graph or _graph()), ws, n, None)
+
+
+BUILDS = [
+    ("cache", lambda: _build(_q8(Hq=30)), INVALID),
+    ("graph", lambda: _build(graph=_graph(S=-1)), INVALID),
+    ("graph T_cap", lambda: _build(graph=_graph(T_cap=8192)), CAPACITY),
+    ("labels", lambda: _build(labels=None), INVALID),
+    ("T below S", lambda: _build(T=3), INVALID),
+    ("T above T_cap", lambda: _build(T=4097, stride=5000), CAPACITY),
+    ("labels stride", lambda: _build(stride=4095), INVALID),
+    ("small ws", lambda: _build(n=1024), WORKSPACE),
+    ("no ws", lambda: _build(ws=None), WORKSPACE),
+]
+
+
+@pytest.mark.parametrize("name,call,status", BUILDS, ids=[b[0] for b in BUILDS])
+def test_build_refusals(name, call, status):
+    assert call() == status, ckv.ckv_last_error()
+    assert ckv.ckv_last_error()
+
+
+@pytest.mark.parametrize("bad", [
+    lambda c, g, lab, ws: ckv.ckv_build_centroids_q8(c, lab.long(), 8, g, ws),
+    lambda c, g, lab, ws: ckv.ckv_build_centroids_q8(c, lab[:3], 8, g, ws),
+    lambda c, g, lab, ws: ckv.ckv_build_centroids_q8(c, lab, 9, g, ws),
+    lambda c, g, lab, ws: ckv.ckv_build_centroids_q8(c, lab.t().contiguous().t(), 8, g, ws),
+    lambda c, g, lab, ws: ckv.ckv_build_centroids_q8(c, lab, 8, g, ws, torch.zeros(3, dtype=torch.int32)),
+    lambda c, g, lab, ws: ckv.ckv_build_centroids_q8(c, lab, 8, g, ws, torch.zeros(2, dtype=torch.bool)),
+    lambda c, g, lab, ws: ckv.ckv_build_centroids_q8(ckv.new_q8_cache(3, 2, 4, 64, 8, 16, 4, device="cpu"), lab, 8, g, ws),
+    lambda c, g, lab, ws: ckv.ckv_build_centroids_q8(c, lab, 8, g, ws),  # not on a GPU
+])
+def test_build_binding_refuses(bad):
+    c = ckv.new_q8_cache(2, 2, 4, 64, 8, 16, 4, device="cpu")
+    g = ckv.new_graph(ckv.q8_shape(c, 64), ckv.PER_GROUP, 0, 4, 4, device="cpu")
+    with pytest.raises(ValueError):
+        bad(c, g, torch.zeros((4, 8), dtype=torch.int32), torch.zeros(1 << 16, dtype=torch.uint8))
 
 
 def test_trim_null_descriptors():
@@ -365,3 +405,117 @@ def test_restored_centres_are_the_oracles():
                 # plus c), each at most 2^-24 of the largest value: 13 of them
                 err = np.abs(g.cent[u, c].double().cpu().numpy() - np.mean(rows, 0)).max()
                 assert err <= 13 * 2.0 ** -24 * np.abs(rows).max()
+
+
+# ---------------------------------------------------------------------------
+# requests of different length
+# ---------------------------------------------------------------------------
+
+def ragged(lens, mode="group", fmt="int8", dtype=torch.float32, d=64, S=4, C=7, block=32, seed=0, T_cap=5024):
+    """A cache of these lengths, filled in one growth, and labels for each request's own positions (behind them: any)."""
+    gen = torch.Generator().manual_seed(seed)
+    B, n = len(lens), sum(lens)
+    cache = ckv.new_q8_cache(B, 2, 4, d, n // block + B + 4, block, 160, fmt, dtype)
+    st = PagedLayerState(cache, mode, S, C, 8, T_cap=T_cap)
+    st.grow(i32(lens), n)
+    st.write(*((torch.randn((n, 2, d), generator=gen) * torch.exp2(torch.randint(-3, 3, (n, 1, 1), generator=gen).float()))
+               .to(dtype).to(DEV) for _ in range(2)))
+    U = st.graph.U
+    labels = torch.randint(0, C, (U, max(lens)), generator=gen, dtype=torch.int32)
+    for u in range(U):
+        labels[u, :S] = -1
+        labels[u, lens[u * B // U]:] = -9  # never looked at
+    return st, labels
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", ["group", "head"])
+@pytest.mark.parametrize("fmt,dtype,d", [("int8", torch.float32, 64), ("e4m3", torch.float32, 128), ("int8", torch.bfloat16, 128)])
+def test_build_over_requests_of_different_length(mode, fmt, dtype, d):
+    """Each request's graph is, bit for bit, what the wide cache's build makes of its own positions; the values held are
+    fp32 whatever the rows' type."""
+    lens = [300, 0, 5000, 3, 17, 4, 4097]
+    st, labels = ragged(lens, mode, fmt, dtype, d)
+    st.build(labels.to(DEV), max(lens))
+    assert ckv.ckv_get_device_error(st.cache) == 0 and int(st.graph.dev_err) == 0
+    c = st.cache
+    f32 = ckv.q8_cache(c.k, c.v, c.k_scale, c.v_scale, c.table, c.len, 4, torch.float32)
+    K, V = (torch.empty((len(lens), 2, 5024, d), device=DEV) for _ in range(2))
+    ckv.ckv_q8_read(f32, K, V)
+    g, G = st.graph, st.graph.U // len(lens)
+    wide = ckv.cache_desc(K, V, 4)
+    for b, n in enumerate(lens):
+        ref = ckv.new_graph(wide, g.desc.mode, min(4, n), 7, 8)
+        ws = ckv.new_workspace(ckv.ckv_workspace_size(wide, ref))
+        own = torch.full(labels.shape, 0, dtype=torch.int32)
+        own[:, : min(4, n)] = -1
+        own[b * G: (b + 1) * G, :n] = labels[b * G: (b + 1) * G, :n]
+        ckv.ckv_build_centroids(wide, own.to(DEV), n, ref, ws)
+        rows = slice(b * G, (b + 1) * G)
+        for f in ("comm_of", "offs", "cnt", "cent", "cent_q", "cent_qs", "num_comm", "tail_len", "built"):
+            assert torch.equal(getattr(ref, f)[rows], getattr(g, f)[rows]), (b, f)
+        m = max(n - 4, 0)
+        assert torch.equal(ref.tok[rows, :m], g.tok[rows, :m])
+    # every token but the sinks is selectable, and nothing else
+    q = torch.randn((len(lens), 4, d), device=DEV).to(dtype)
+    st.select(q, 10 ** 6)
+    for u in range(g.U):
+        n = lens[u // G]
+        assert sorted(st.sel.sel_tok[u, : int(st.sel.n_tok[u])].tolist()) == list(range(max(n, 4)))
+
+
+@pytest.mark.gpu
+def test_build_of_some_requests_leaves_the_others():
+    """A request ends, another takes its row and is built alone; the others decode on."""
+    b = Batch()
+    b.step([1, 1, 1])
+    before = b.state()
+    b.st.grow(i32([0, -10 ** 6, 0]), 0)
+    n = 37
+    b.st.grow(i32([0, n, 0]), n)
+    gen = torch.Generator().manual_seed(9)
+    rows = torch.randn((2, n, 2, b.d), generator=gen).to(DEV)
+    b.st.write(rows[0], rows[1])
+    labels = torch.full((b.st.graph.U, 64), 10 ** 6, dtype=torch.int32)
+    mine = list(range(b.G, 2 * b.G))
+    labels[mine, :n] = torch.randint(0, b.C, (b.G, n), generator=gen, dtype=torch.int32)
+    labels[mine, : b.S] = -1
+    b.st.build(labels.to(DEV), requests=i32([0, 5, 0]))
+    same(before, b.state(), [u for u in range(3 * b.G) if u not in mine])
+    assert b.st.graph.built.tolist() == [90] * b.G + [n] * b.G + [90] * b.G
+    for _ in range(2):
+        p, _ = b.step([1, 1, 1])
+        assert p.granted.tolist() == [1, 1, 1]
+        b.check_lists()
+    assert int(b.st.assigned.min()) >= 0 and b.errors() == (0, 0)
+
+
+@pytest.mark.gpu
+def test_build_flags_what_it_cannot_use():
+    lens = [100, 60, 80]
+    st, labels = ragged(lens, block=16, T_cap=160)
+    g, G, c = st.graph, 2, st.cache
+    st.build(labels[:, :90].contiguous().to(DEV))  # request 0 is longer than its labels
+    assert int(g.dev_err) == ckv.DEVERR_LABEL_RANGE and ckv.ckv_get_device_error(c) == 0
+    assert g.built.tolist() == [90] * G + [60] * G + [80] * G and g.cnt.sum(1).tolist() == [86] * G + [56] * G + [76] * G
+    g.dev_err.zero_()
+    st.build(labels.to(DEV))
+    whole = [x.clone() for x in (g.cnt, g.cent)]
+    assert int(g.dev_err) == 0
+    c.len[1] = -5
+    c.table[2, 1] = 10 ** 6  # positions 16..31 of request 2
+    st.build(labels.to(DEV))
+    assert ckv.ckv_get_device_error(c, reset=True) == ckv.DEVERR_BLOCK and int(g.dev_err) == 0
+    assert torch.equal(whole[0][:G], g.cnt[:G]) and torch.equal(whole[1][:G], g.cent[:G])
+    assert not g.cnt[G: 2 * G].any() and g.built[G: 2 * G].tolist() == [0] * G
+    k, _ = st.read(80)  # zeros at those positions
+    assert ckv.ckv_get_device_error(c, reset=True) == ckv.DEVERR_BLOCK
+    for u in range(2 * G, 3 * G):
+        rows = k[2, u % 2].double().cpu()
+        for cc in range(7):
+            at = (labels[u, :80] == cc).nonzero().flatten()
+            if len(at):  # one rounding of the mean
+                assert (g.cent[u, cc].double().cpu() - rows[at].mean(0)).abs().max() <= 2.0 ** -24 * rows.abs().max()
+    c.len[1] = 160 * 16 + 1
+    st.build(labels.to(DEV), requests=i32([1, 0, 0]))  # requests left out are not looked at
+    assert ckv.ckv_get_device_error(c) == 0
