@@ -141,21 +141,35 @@ __device__ __forceinline__ float2 unpack_half2(unsigned w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+// w m + a for a pair of fp16 (m and a their bits)
+__device__ __forceinline__ unsigned half2_fma(unsigned w, unsigned short m, unsigned short a) {
+    const __half2 x = __hfma2(*reinterpret_cast<const __half2*>(&w),
+                              __halves2half2(__ushort_as_half(m), __ushort_as_half(m)),
+                              __halves2half2(__ushort_as_half(a), __ushort_as_half(a)));
+    return *reinterpret_cast<const unsigned*>(&x);
+}
+
 // A K word's four codes as two fp16 pairs, in an order of their own (K_PAIR).
-// int8: bytes 0, 2 and 1, 3, biased by 128, as fp16 subnormals (128 + c) 2^-24:
-// three instructions for four codes.  The bias leaves through the
-// accumulators' start, -128 2^-24 sum q.  e4m3: bytes 0, 1 and 2, 3.
+// int8: bytes 0, 2 and 1, 3; flipped to 128 + c they are the fp16 subnormals (128 + c)
+// 2^-24, and times 2^15 less 2^-2 that is c 2^-9, exact: five instructions for four
+// codes.  The products' sums are then of the size of sum |q c|.  (With the bias left in,
+// and taken off through the accumulators' start, they would be 128 sum |q| large
+// whatever the codes are, and the tensor core truncates them: 12 to 50 times the error
+// of the scores where most codes are small, as beside a large channel's.  Codes as
+// subnormals, c 2^-24, give 5 times: it aligns them like normal numbers of the least
+// exponent.  The two instructions cost 0 to 4 % of a call.)  e4m3: bytes 0, 1 and 2, 3.
 template <int FMT>
 __device__ __forceinline__ void q8_k_halves(unsigned w, unsigned& p0, unsigned& p1) {
     if constexpr (FMT == Q8_I8) {
         w ^= 0x80808080u;
-        p0 = w & 0x00ff00ffu;
-        p1 = __byte_perm(w, 0u, 0x4341);
+        p0 = half2_fma(w & 0x00ff00ffu, 0x7800, 0xb400);
+        p1 = half2_fma(__byte_perm(w, 0u, 0x4341), 0x7800, 0xb400);
     } else {
         p0 = e4m3x2_half2((unsigned short)(w & 0xffffu));
         p1 = e4m3x2_half2((unsigned short)(w >> 16));
     }
 }
+template <int FMT> constexpr float K_UNIT = FMT == Q8_I8 ? 0x1p9f : 1.f;  // a K code of 1 enters the products as 1 / K_UNIT
 // Dims of a word's fp16 pairs: pair i holds dims first(i) and first(i) + step.
 template <int FMT> struct KPair {
     static constexpr int step = FMT == Q8_I8 ? 2 : 1;
@@ -163,8 +177,8 @@ template <int FMT> struct KPair {
 };
 
 // The words of two tokens (a, b), four dims each: h[i] = fp16 (a_i, b_i).  int8: a
-// byte flipped to 128 + c is the low part of an fp16 in [1024, 1280), whose step is 1;
-// here the bias is taken off (in the sums it would cancel 2^7 of their bits).
+// byte flipped to 128 + c is the low part of an fp16 in [1024, 1280), whose step is 1,
+// and 1152 comes off again.
 template <int FMT>
 __device__ __forceinline__ void q8_v_halves(unsigned a, unsigned b, unsigned (&h)[4]) {
     if constexpr (FMT == Q8_I8) {
@@ -205,15 +219,16 @@ __device__ __forceinline__ void cp_async_4p(unsigned s, const void* g, bool pred
                  : "memory");
 }
 
-// The state of one warp over one unit's tokens: lane 4 g + t.
-template <int D, int GQ, int FMT, int NH>
+// The state of one warp over one unit's tokens: lane 4 g + t.  QLO: q may have lo
+// parts (with 8 heads a group they take registers and products of their own, which
+// bf16 rows, exact in one fp16, do without; with fewer heads nothing).
+template <int D, int GQ, int FMT, int NH, bool QLO>
 struct Q8Warp {
     using QG = Q8Geom<D, NH>;
     static constexpr bool SPLIT = GQ == 8;  // hi and lo in products of their own
     unsigned qh[QG::KS][2];                 // Q^T fragments (SPLIT: hi; else hi in columns 0..3, lo or hi again in 4..7)
-    unsigned ql[SPLIT ? QG::KS : 1][2];
+    unsigned ql[SPLIT && QLO ? QG::KS : 1][2];
     bool q_lo;                              // some lo is not zero (q in fp32)
-    float s0[2];                            // start of the scores' accumulators (int8: the codes' bias taken off)
     float qf[2];                            // per head of this lane: 2^e log2(e)/sqrt(d)
     float m0[2], mw[2], c[2], l[2];         // references of x and of x + log2 s_v, weight factor, sum
     f32x2 o[QG::MT][2];                     // columns 2t, 2t + 1 of rows g and g + 8 of each 16-dim tile
@@ -278,7 +293,6 @@ struct Q8Warp {
         const float down = __uint_as_float((unsigned)(127 - e) << 23);
         const float f = __uint_as_float((unsigned)(127 + e) << 23) * scale_log2;
         using KP = KPair<FMT>;
-        float sum = 0.f;
 #pragma unroll
         for (int s = 0; s < QG::KS; ++s)
 #pragma unroll
@@ -289,7 +303,7 @@ struct Q8Warp {
             }
         // bf16 rows are exact in one fp16; without lo parts columns 4..7 repeat 0..3,
         // and no lane has to fetch the scores of its weights' heads
-        q_lo = dtype == CKV_DTYPE_F32;
+        q_lo = QLO && dtype == CKV_DTYPE_F32;
         if (q_lo) {
 #pragma unroll
             for (int s = 0; s < QG::KS; ++s)
@@ -297,34 +311,12 @@ struct Q8Warp {
                 for (int i = 0; i < 2; ++i) {
                     const float2 h2 = unpack_half2(qh[s][i]);
                     const unsigned lo = pack_half2(x[s][KP::second * i] - h2.x, x[s][KP::second * i + KP::step] - h2.y);
-                    if constexpr (SPLIT) ql[s][i] = lo;
-                    else if (g >= 4) qh[s][i] = lo;
+                    if constexpr (SPLIT && QLO) ql[s][i] = lo;
+                    else if (!SPLIT && g >= 4) qh[s][i] = lo;
                 }
         }
-        if constexpr (FMT == Q8_I8) {
 #pragma unroll
-            for (int s = 0; s < QG::KS; ++s)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float2 h2 = unpack_half2(qh[s][i]);
-                    sum += h2.x + h2.y;
-                    if (SPLIT && q_lo) {
-                        const float2 l2 = unpack_half2(ql[SPLIT ? s : 0][i]);
-                        sum += l2.x + l2.y;
-                    }
-                }
-            sum += __shfl_xor_sync(FULL, sum, 1);
-            sum += __shfl_xor_sync(FULL, sum, 2);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            qf[k] = __shfl_sync(FULL, f, head(t, k) * 4);
-            s0[k] = 0.f;
-            if constexpr (FMT == Q8_I8) {
-                s0[k] = -0x1p-17f * __shfl_sync(FULL, sum, (2 * t + k) * 4);
-                qf[k] *= 0x1p24f;
-            }
-        }
+        for (int k = 0; k < 2; ++k) qf[k] = __shfl_sync(FULL, f, head(t, k) * 4) * K_UNIT<FMT>;
     }
     __device__ __forceinline__ static const void* q_row(const void* q, int dtype, size_t row) {
         return static_cast<const char*>(q) + row * D * (dtype == CKV_DTYPE_BF16 ? 2 : 4);
@@ -350,7 +342,7 @@ struct Q8Warp {
         float s[NH][2][2];  // [half][token g | g + 8][head]
 #pragma unroll
         for (int j = 0; j < NH; ++j) {
-            float sa[4] = {s0[0], s0[1], s0[0], s0[1]}, sb[4];
+            float sa[4], sb[4];
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
                 const uint4 ka = j ? lds128<QG::HALF>(i ? ks2 : ks) : lds128<0>(i ? ks2 : ks);
@@ -362,9 +354,9 @@ struct Q8Warp {
                     unsigned a0, a1, a2, a3;
                     q8_k_halves<FMT>(wa[w], a0, a2);
                     q8_k_halves<FMT>(wb[w], a1, a3);
-                    if (k == 1) q8_mma0(sb, a0, a1, a2, a3, qh[k][0], qh[k][1]);
+                    if (k <= 1) q8_mma0(k ? sb : sa, a0, a1, a2, a3, qh[k][0], qh[k][1]);
                     else q8_mma((w & 1) ? sb : sa, a0, a1, a2, a3, qh[k][0], qh[k][1]);
-                    if constexpr (SPLIT) {
+                    if constexpr (SPLIT && QLO) {
                         if (q_lo) q8_mma((w & 1) ? sb : sa, a0, a1, a2, a3, ql[k][0], ql[k][1]);
                     }
                 }

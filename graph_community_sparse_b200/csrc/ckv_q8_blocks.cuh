@@ -228,11 +228,11 @@ __device__ __forceinline__ void copy_half(unsigned sm, const char* k, const char
     }
 }
 
-template <int D, int GQ, int FMT, bool LIST, bool NBR>
+template <int D, int GQ, int FMT, bool LIST, bool NBR, bool QLO>
 __global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_kernel(const __grid_constant__ BlocksQ8Params p) {
     using SH = QdShape<D, LIST>;
     using QG = Q8Geom<D, SH::NH>;
-    using W = Q8Warp<D, GQ, FMT, SH::NH>;
+    using W = Q8Warp<D, GQ, FMT, SH::NH, QLO>;
     using SM = BlocksQ8Smem<D, GQ, LIST>;
     constexpr int STAGES = SH::STAGES, TOK = SH::TOK;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -587,10 +587,10 @@ __global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_
 }
 
 // Resident blocks, but no more than there can be pieces (`most`).
-template <int D, int GQ, int FMT, bool LIST, bool NBR = false>
-static cudaError_t launch_blocks_q8_t(const BlocksQ8Params& p, long long most, cudaStream_t st) {
+template <int D, int GQ, int FMT, bool LIST, bool NBR, bool QLO>
+static cudaError_t launch_blocks_q8_q(const BlocksQ8Params& p, long long most, cudaStream_t st) {
     static LaunchCache lc;
-    auto kern = blocks_q8_kernel<D, GQ, FMT, LIST, NBR>;
+    auto kern = blocks_q8_kernel<D, GQ, FMT, LIST, NBR, QLO>;
     const size_t smem = BlocksQ8Smem<D, GQ, LIST>::FIXED + (size_t)(LIST ? p.U : p.c.t.B) * 4;
     int per_sm = 0, sms = 0;
     cudaError_t e = prepare_launch(kern, lc, smem, QD_THREADS, &per_sm, &sms);
@@ -598,6 +598,14 @@ static cudaError_t launch_blocks_q8_t(const BlocksQ8Params& p, long long most, c
     if (sms <= 0 || per_sm <= 0) return cudaErrorInvalidConfiguration;
     const int grid = (int)min((long long)min(sms * per_sm, QD_MAX_GRID), most);
     return launch_pdl(KK_ATTENTION, kern, dim3(grid), dim3(QD_THREADS), smem, st, p);
+}
+
+template <int D, int GQ, int FMT, bool LIST, bool NBR = false>
+static cudaError_t launch_blocks_q8_t(const BlocksQ8Params& p, long long most, cudaStream_t st) {
+    if constexpr (GQ == 8) {
+        if (p.c.dtype == CKV_DTYPE_BF16) return launch_blocks_q8_q<D, GQ, FMT, LIST, NBR, false>(p, most, st);
+    }
+    return launch_blocks_q8_q<D, GQ, FMT, LIST, NBR, true>(p, most, st);
 }
 
 // The workspace's parts after its head: the units' counters, the partials, then the

@@ -1,0 +1,124 @@
+"""The 8-bit attention's arithmetic over the range of its formats: what the bounds of the other tests are too wide to
+see.  Scores where one channel of the keys is large, scales that differ by more than fp32's exponents, values that are not
+finite behind small weights, and the size of the rounding errors themselves."""
+import math
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import graph_community_sparse_b200 as ckv
+import q8_ref as Q
+from parity_util import check_neighbours
+
+DEV = "cuda"
+
+
+def i32(x):
+    return torch.tensor(list(x), dtype=torch.int32, device=DEV)
+
+
+def pool(lens, Hkv, gq, d, block, fmt, dtype, seed=0):
+    """Requests of these lengths in a pool of zeros, blocks in random order; scales of 1/100."""
+    nb = [-(-n // block) for n in lens]
+    cache = ckv.new_q8_cache(len(lens), Hkv, Hkv * gq, d, sum(nb) + 2, block, max(nb + [1]), fmt, dtype)
+    ids = list(range(sum(nb) + 2))
+    random.Random(seed).shuffle(ids)
+    for b, n in enumerate(nb):
+        cache.table[b, :n] = i32([ids.pop() for _ in range(n)])
+    cache.len.copy_(i32(lens))
+    cache.k_scale.fill_(0.01)
+    cache.v_scale.fill_(0.01)
+    return cache
+
+
+def put(cache, which, b, values):
+    """Codes [n, Hkv, d] of request b."""
+    t, n, bs = getattr(cache, which), values.shape[0], cache.desc.blocks.block
+    ids = cache.table[b].tolist()
+    for j in range(0, n, bs):
+        t[ids[j // bs], :, : min(bs, n - j)] = values[j: j + bs].transpose(0, 1).to(DEV).to(t.dtype)
+
+
+def held(cache, b, h):
+    """K and V values of request b, head h, in float64 [n, d]."""
+    n, bs = int(cache.len[b]), cache.desc.blocks.block
+    ids = cache.table[b, : -(-n // bs)].long()
+    out = []
+    for t, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        x = t[ids, h].float().double() * s[ids, h].double()[:, None, None]
+        out.append(x.reshape(-1, t.shape[-1])[:n].cpu().numpy())
+    return out
+
+
+def every_way(cache, q, S=0, neighbours=False):
+    """The outputs of the dense call and of lists of all tokens in random order (one a KV head, one a query head), and
+    the last one's lists and neighbours."""
+    B = cache.B
+    outs, lists, nbr = [], None, None
+    out = torch.full(q.shape, float("nan"), device=DEV)
+    ckv.ckv_dense_decode_q8(cache, q, out, ckv.new_workspace(ckv.ckv_q8_workspace_size(cache)))
+    outs.append(out)
+    lens = cache.len.tolist()
+    for mode in (ckv.PER_HEAD, ckv.PER_GROUP):
+        shape = ckv.q8_shape(cache, max(lens))
+        graph = ckv.new_graph(shape, mode, S, 1, 0)
+        sel = ckv.new_selection(shape, graph, max(lens))
+        G = graph.U // B
+        lists = [random.Random(u).sample(range(lens[u // G]), lens[u // G]) for u in range(graph.U)]
+        for u, x in enumerate(lists):
+            sel.sel_tok[u, : len(x)] = i32(x)
+        sel.n_tok.copy_(i32([len(x) for x in lists]))
+        out = torch.full(q.shape, float("nan"), device=DEV)
+        nbr = torch.empty((graph.U, 8), dtype=torch.int32, device=DEV) if neighbours else None
+        ckv.ckv_sparse_decode_q8(cache, q, graph, sel, out, nbr,
+                                 ckv.new_workspace(ckv.ckv_q8_workspace_size(cache, graph, sel)))
+        outs.append(out)
+    return outs, lists, nbr
+
+
+def score_share(S):
+    """The part of a weight's relative error that its score brings: q and the codes are exact in fp16 (bf16 q), at most
+    d/16 = 8 products of 16 terms are added with an error of 2^-23 of the largest sum each (two chains of four, a
+    truncating accumulator), then the chains' sum, the scale's two products and the subtraction: 14 * 2^-23 S, with S the
+    largest sum of |q_i k_i| / sqrt(d)."""
+    return 14 * 2.0 ** -23 * S
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("d,gq", [(128, 4), (128, 8), (64, 1), (64, 2), (64, 8)])
+@pytest.mark.parametrize("nonzeros", [1, 4, 60])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_weights_beside_a_large_channel(fmt, d, gq, nonzeros, dtype):
+    """One channel of the keys takes the codes' whole range and q is zero there; a few others are 1 or -1 and the rest 0.
+    V is the identity, so that the output is the weights themselves: their errors follow the scores' sums of |q k|, not
+    the codes' range."""
+    n, gen = d, torch.Generator().manual_seed(d + gq + nonzeros)
+    cache = pool([n], 1, gq, d, 16, fmt, dtype)
+    put(cache, "v", 0, 100 * torch.eye(n)[:, None, :])
+    cache.k_scale.fill_(16.0)
+    for again in range(8):
+        k = torch.zeros((n, 1, d))
+        at = torch.rand((n, 1, d), generator=gen).topk(nonzeros, -1).indices
+        k.scatter_(2, at, 1.0 - 2 * torch.randint(0, 2, (n, 1, nonzeros), generator=gen).float())
+        k[:, 0, 5] = 120.0
+        put(cache, "k", 0, k)
+        q = torch.randn((1, gq, d), generator=gen).bfloat16().to(dtype)  # exact in one fp16 term, whatever the type
+        q[:, :, 5] = 0.0
+        q = q.to(DEV)
+        outs, lists, nbr = every_way(cache, q, neighbours=True)
+        K, V = held(cache, 0, 0)
+        for h in range(gq):
+            want, S = Q.attention(q[0, h].double().cpu().numpy(), K, V)
+            # beside the scores: exp2 2^-22, a weight in two fp16 terms 2^-22 (from 2^-6 of the largest on), scale
+            # products 2^-23, and the weights' sum over 5 tiles, 8 lanes and 4 warps; numerator and denominator
+            rel = 2 * (score_share(S) + 2 * 2.0 ** -22 + 2.0 ** -23 * (1 + 5 + 8 + 4))
+            large = want >= want.max() / 64
+            for out in outs:
+                err = np.abs(out[0, h].double().cpu().numpy() / want - 1)[large].max()
+                assert err <= rel, (again, h, err, rel)
+        qn = q[0].double().cpu().numpy()
+        S = (np.abs(K) @ np.abs(qn).T).max() / math.sqrt(d)
+        check_neighbours(nbr[0].tolist(), qn, K, np.asarray(lists[0]), 0, band=2 * score_share(S))
