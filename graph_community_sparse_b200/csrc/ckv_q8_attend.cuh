@@ -149,6 +149,13 @@ __device__ __forceinline__ unsigned half2_fma(unsigned w, unsigned short m, unsi
     return *reinterpret_cast<const unsigned*>(&x);
 }
 
+// the smaller of the two, NaN if either is
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // A K word's four codes as two fp16 pairs, in an order of their own (K_PAIR).
 // int8: bytes 0, 2 and 1, 3; flipped to 128 + c they are the fp16 subnormals (128 + c)
 // 2^-24, and times 2^15 less 2^-2 that is c 2^-9, exact: five instructions for four
@@ -426,7 +433,7 @@ struct Q8Warp {
                 for (int r = 0; r < NS; ++r)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        cv[j][r][e] = fminf(c[e] * vs[j][r], 0x1p127f);  // finite: a weight of zero stays one
+                        cv[j][r][e] = min_nan(c[e] * vs[j][r], 0x1p127f);  // not inf: a weight of zero stays one; NaN stays
                         wide = wide || cv[j][r][e] > 128.f;
                     }
 #pragma unroll

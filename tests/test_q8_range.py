@@ -122,3 +122,28 @@ def test_weights_beside_a_large_channel(fmt, d, gq, nonzeros, dtype):
         qn = q[0].double().cpu().numpy()
         S = (np.abs(K) @ np.abs(qn).T).max() / math.sqrt(d)
         check_neighbours(nbr[0].tolist(), qn, K, np.asarray(lists[0]), 0, band=2 * score_share(S))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("d,gq", [(64, 4), (128, 8), (64, 1)])
+@pytest.mark.parametrize("score", [0.0, -80.0, -300.0])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_not_finite_blocks_reach_the_output_behind_any_weight(fmt, d, gq, score, which):
+    """A block whose scale is NaN, for K or V of one head, makes its request's outputs of that head NaN, even where its
+    tokens weigh 2^-115 or nothing in fp32; no other output."""
+    n = 100
+    cache = pool([n, n], 2, gq, d, 16, fmt, torch.float32)
+    k = torch.zeros((n, 2, d))
+    k[48:64, :, 3] = -96.0
+    for b in range(2):
+        put(cache, "k", b, k)
+        put(cache, "v", b, torch.full((n, 2, d), 5.0))
+    at = int(cache.table[0, 3])
+    cache.k_scale[at] = -score * math.sqrt(d) / 96
+    (cache.k_scale if which == "k" else cache.v_scale)[at, 1] = float("nan")
+    q = torch.zeros((2, 2 * gq, d), device=DEV)
+    q[:, :, 3] = 1.0
+    for out in every_way(cache, q)[0]:
+        assert torch.isnan(out[0, gq:]).all()
+        assert torch.isfinite(out[0, :gq]).all() and torch.isfinite(out[1]).all()
