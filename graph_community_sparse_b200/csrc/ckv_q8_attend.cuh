@@ -477,11 +477,15 @@ struct Q8Warp {
                 const float mn = fmaxf(m0[e], mx);
                 mw[e] = fmaxf(mw[e], mv);
                 const int k2 = (int)fminf(fmaxf(5.f - ceilf(mw[e] - mn), -120.f), 120.f);
-                const float cn = __uint_as_float((unsigned)(127 + k2) << 23);
+                const int up = k2 + 127 - (int)(__float_as_uint(c[e]) >> 23);  // c grows by 2^up
                 const float f = exp2_approx(m0[e] - mn);
-                fo[e] = f * (cn / c[e]);
+                // the factor of what is summed so far is at most 2.  Where c grows by more
+                // than 2^100 (V scales that fall while the scores jump) f may be zero and 2^up
+                // infinite: in one exponent there
+                fo[e] = up > 100 ? exp2_approx(m0[e] - mn + (float)up)
+                                 : f * __uint_as_float((unsigned)(127 + max(up, -126)) << 23);
                 m0[e] = mn;
-                c[e] = cn;
+                c[e] = __uint_as_float((unsigned)(127 + k2) << 23);
                 l[e] *= f;
             }
             const f32x2 f2 = pack2(fo[0], fo[1]);

@@ -52,9 +52,9 @@ def held(cache, b, h):
     return out
 
 
-def every_way(cache, q, S=0, neighbours=False):
-    """The outputs of the dense call and of lists of all tokens in random order (one a KV head, one a query head), and
-    the last one's lists and neighbours."""
+def every_way(cache, q, S=0, neighbours=False, shuffle=True):
+    """The outputs of the dense call and of lists of all tokens, in random order or in theirs (one a query head, one a KV
+    head), and the last one's lists and neighbours."""
     B = cache.B
     outs, lists, nbr = [], None, None
     out = torch.full(q.shape, float("nan"), device=DEV)
@@ -66,7 +66,8 @@ def every_way(cache, q, S=0, neighbours=False):
         graph = ckv.new_graph(shape, mode, S, 1, 0)
         sel = ckv.new_selection(shape, graph, max(lens))
         G = graph.U // B
-        lists = [random.Random(u).sample(range(lens[u // G]), lens[u // G]) for u in range(graph.U)]
+        lists = [random.Random(u).sample(range(lens[u // G]), lens[u // G]) if shuffle else list(range(lens[u // G]))
+                 for u in range(graph.U)]
         for u, x in enumerate(lists):
             sel.sel_tok[u, : len(x)] = i32(x)
         sel.n_tok.copy_(i32([len(x) for x in lists]))
@@ -147,3 +148,35 @@ def test_not_finite_blocks_reach_the_output_behind_any_weight(fmt, d, gq, score,
     for out in every_way(cache, q)[0]:
         assert torch.isnan(out[0, gq:]).all()
         assert torch.isfinite(out[0, :gq]).all() and torch.isfinite(out[1]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("d,gq", [(64, 4), (128, 8), (128, 1)])
+@pytest.mark.parametrize("v_scales", [(2.0 ** 14, 0.0), (2.0 ** 60, 2.0 ** -107 / 127), (2.0 ** 90, 1.0), (0.0, 2.0 ** 14),
+                                      (2.0 ** -100, 2.0 ** 100)])
+def test_v_scales_that_fall_or_rise_where_the_scores_jump(fmt, d, gq, v_scales):
+    """A request whose second half scores 150 to 300 (in powers of two) above its first, and whose V scale there is that
+    much smaller, zero or larger: finite, and the second half's values."""
+    n = 192  # one block's warps see tiles of the first half, then of the second
+    cache = pool([n], 1, gq, d, 32, fmt, torch.float32)
+    k = torch.zeros((n, 1, d))
+    k[96:, :, 0] = 64.0
+    put(cache, "k", 0, k)
+    gen = torch.Generator().manual_seed(1)
+    put(cache, "v", 0, torch.randint(-60, 61, (n, 1, d), generator=gen).float().div(8).round().mul(8))
+    for j in range(6):
+        cache.v_scale[int(cache.table[0, j])] = v_scales[j // 3]
+    for step in (150.0, 300.0):
+        cache.k_scale.fill_(step * math.log(2) * math.sqrt(d) / 64)
+        q = torch.zeros((1, gq, d), device=DEV)
+        q[:, :, 0] = 1.0
+        K, V = held(cache, 0, 0)
+        want = V[96:].mean(0)  # equal weights; the first half's are 2^-150 of them or less
+        rest = 2.0 ** -step * np.abs(V[:96]).max()
+        # 96 equal weights: each and their sums off by at most 2^-21 (exp2, two fp16 terms, scale products, sums over
+        # 3 tiles and 4 warps), twice for numerator and denominator
+        tol = 2 * 2.0 ** -21 * np.abs(V[96:]).max() + 2 * rest
+        for out in every_way(cache, q, shuffle=False)[0]:
+            assert torch.isfinite(out).all()
+            assert np.abs(out.double().cpu().numpy() - want).max() <= tol
