@@ -575,8 +575,8 @@ ckv_status ckv_q8_read(const ckv_q8_desc* cache, const int32_t* first, int32_t R
     if (R == 0) return ok();
     CKV_TRY(check_rows(cache, k_out, v_out, stride_b, stride_t, stride_h));
     if (stride_t < cache->d) return fail(CKV_ERR_INVALID_ARG, "stride_t < d: rows would overlap");
-    if (R > 1 << 30 || (int64_t)cache->blocks.B * cache->Hkv * (((int64_t)R + 31) / 32) > 0x7fffffffll)
-        return fail(CKV_ERR_UNSUPPORTED, "R above 2^30 or B * Hkv * R above 2^36");
+    if (R > 1 << 30 || ckv::q8_read_blocks(cache->blocks.B, cache->Hkv, cache->d, R) > 0x7fffffffll)
+        return fail(CKV_ERR_UNSUPPORTED, "R above 2^30 or B * Hkv * ceil(R d / 2048) above 2^31 - 1");
     ckv::RowsView rv{k_out, v_out, stride_b, stride_t, stride_h, 0};
     return cuda_status(ckv::launch_q8_read(q8_view(cache), first, R, rv, reinterpret_cast<cudaStream_t>(stream)),
                        "ckv_q8_read");

@@ -44,6 +44,13 @@ struct RowsView {  // new rows in, or read-back rows out
 
 cudaError_t launch_plan_blocks(const TableView& t, const int32_t* add, const PlanView& p, cudaStream_t st);
 cudaError_t launch_quant_append(const Q8View& c, const PlanView& p, const RowsView& r, cudaStream_t st);
+// A block of the read takes READ_PASS rows a thread, D / 8 threads to a row.
+constexpr int READ_THREADS = 128;
+constexpr int READ_PASS = 2;
+constexpr int q8_read_rows(int d) { return READ_THREADS / (d / 8) * READ_PASS; }
+constexpr long long q8_read_blocks(int B, int Hkv, int d, long long R) {
+    return (R + q8_read_rows(d) - 1) / q8_read_rows(d) * B * Hkv;
+}
 cudaError_t launch_q8_read(const Q8View& c, const int32_t* first, int R, const RowsView& r, cudaStream_t st);
 // The attention's workspace: after the head, counters of the units (of the most there
 // can be, so that they are in the same place for every cache), the partials, and the

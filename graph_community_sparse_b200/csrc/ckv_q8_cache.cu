@@ -537,9 +537,6 @@ cudaError_t launch_quant_append(const Q8View& c, const PlanView& p, const RowsVi
 // to 45, whose stores leave half sectors); up to 1000 rows each of 13 requests 5.8 us
 // (7.3 with 256 threads of 4 passes: fewer, longer blocks).
 // ---------------------------------------------------------------------------
-constexpr int READ_THREADS = 128;
-constexpr int READ_PASS = 2;
-
 struct ReadParams {
     Q8View c;
     RowsView r;
@@ -621,10 +618,8 @@ __global__ void __launch_bounds__(READ_THREADS) read_kernel(const __grid_constan
 
 template <typename T, int D, int FMT>
 static cudaError_t launch_read_t(ReadParams q, cudaStream_t st) {
-    constexpr int ROWS = READ_THREADS / (D / 8) * READ_PASS;
-    q.chunks = (q.R + ROWS - 1) / ROWS;
-    const long long grid = (long long)q.chunks * q.c.t.B * q.c.Hkv;
-    if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+    q.chunks = (q.R + q8_read_rows(D) - 1) / q8_read_rows(D);
+    const long long grid = q8_read_blocks(q.c.t.B, q.c.Hkv, D, q.R);  // below 2^31: checked by the caller
     return launch_pdl(KK_UPDATE, read_kernel<T, D, FMT>, dim3((unsigned)grid), dim3(READ_THREADS), 0, st, q);
 }
 

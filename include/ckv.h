@@ -520,7 +520,7 @@ CKV_API ckv_status ckv_quant_append(const ckv_q8_desc* cache, const ckv_plan_des
  * request b, head h is position first[b] + r (first NULL: 0) and goes to
  * k_out + b * stride_b + h * stride_h + r * stride_t; positions outside
  * [0, len[b]) give zeros.  16-byte aligned rows; strides in elements; R <= 2^30,
- * B * Hkv * R <= 2^36.
+ * B * Hkv * ceil(R d / 2048) < 2^31.
  */
 CKV_API ckv_status ckv_q8_read(const ckv_q8_desc* cache, const int32_t* first, int32_t R, void* k_out, void* v_out,
                                int64_t stride_b, int64_t stride_h, int64_t stride_t, ckv_stream_t stream);

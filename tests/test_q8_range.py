@@ -1,6 +1,7 @@
 """The 8-bit attention's arithmetic over the range of its formats: what the bounds of the other tests are too wide to
 see.  Scores where one channel of the keys is large, scales that differ by more than fp32's exponents, values that are not
 finite behind small weights, and the size of the rounding errors themselves."""
+import ctypes
 import math
 import random
 
@@ -11,6 +12,8 @@ import torch
 import graph_community_sparse_b200 as ckv
 import q8_ref as Q
 from parity_util import check_neighbours
+from test_abi import FAKE, UNSUPPORTED
+from test_q8_abi import _q8, _table
 
 DEV = "cuda"
 
@@ -180,3 +183,17 @@ def test_v_scales_that_fall_or_rise_where_the_scores_jump(fmt, d, gq, v_scales):
         for out in every_way(cache, q, shuffle=False)[0]:
             assert torch.isfinite(out).all()
             assert np.abs(out.double().cpu().numpy() - want).max() <= tol
+
+
+# ---------------------------------------------------------------------------
+# sizes of the read, without a GPU
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hkv", [(512, 8), (8192, 1), (1023, 8)])
+def test_read_sizes_past_the_grid_are_refused(d, B, Hkv):
+    """Past the documented bound, B Hkv ceil(R d / 2048) < 2^31, the host refuses (nothing is launched)."""
+    cache = _q8(_table(B=B, n_blocks=100), Hkv=Hkv, Hq=4 * Hkv, d=d)
+    for R in (-(-2 ** 31 // (B * Hkv)) * (2048 // d), 2 ** 30):
+        assert ckv.lib.ckv_q8_read(ctypes.byref(cache), None, R, FAKE, FAKE, 0, 0, d, None) == UNSUPPORTED
+        assert "2^31" in ckv.ckv_last_error()
