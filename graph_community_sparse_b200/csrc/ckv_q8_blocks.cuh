@@ -75,7 +75,7 @@ struct BlocksQ8Params {
     float* out;
     float scale_log2;
     // LIST: U units, G per request
-    int U, G, per_head, tok_cap;
+    int U, G, per_head, S, tok_cap;
     const int32_t* sel_tok;
     const int32_t* n_tok;
     float* lam;   // NBR: [U, tok_cap] graph logit of every entry, -inf where it is skipped
@@ -458,6 +458,11 @@ __global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_
         auto position = [&](int w) { return 2 * w + (lane >> 4) < nit && entry(w) < n ? toks[entry(w)] : -1; };
         auto inside = [&](int pos) { return pos >= 0 && pos < len; };
         auto list_block = [&](int pos) { return inside(pos) ? table[pos >> t.sh] : -1; };
+        // every list starts with the sinks, also that of a request too short to hold them
+        auto missing_sink = [&](int e, int pos) {
+            const int held = t.len[seq];
+            return e < p.S && pos == e && held >= 0 && held <= e;
+        };
         int pos0 = 0, pos1 = 0, id0 = 0, row_cur = -1;  // row_cur: the entry's row of the pool; -1: not attended
         // the tiles' scales (lanes 0..15 K's, 16..31 V's) and masks, newest first
         float scales[STAGES];
@@ -479,7 +484,7 @@ __global__ void __launch_bounds__(QD_THREADS, QdShape<D, LIST>::CTAS) blocks_q8_
                     row_cur = -1;
                     if (inside(pos0) && (unsigned)id0 < (unsigned)t.n_blocks)
                         row_cur = ((id0 * Hkv + kvh) << t.sh) + (pos0 & (bs - 1));
-                    else if (x + (lane >> 4) < nit && entry(x >> 1) < n)
+                    else if (x + (lane >> 4) < nit && entry(x >> 1) < n && !missing_sink(entry(x >> 1), pos0))
                         atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
                     pos0 = pos1;
                     id0 = list_block(pos0);

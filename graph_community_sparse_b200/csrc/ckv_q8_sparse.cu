@@ -111,6 +111,7 @@ cudaError_t launch_sparse_decode_q8(const Q8View& c, const GraphView& g, const S
     b.U = c.t.B * g.G;
     b.G = g.G;
     b.per_head = g.mode == CKV_GRAPH_PER_HEAD;
+    b.S = g.S;
     b.tok_cap = s.tok_cap;
     b.sel_tok = s.sel_tok;
     b.n_tok = s.n_tok;

@@ -551,7 +551,8 @@ CKV_API ckv_status ckv_dense_decode_q8(const ckv_q8_desc* cache, const void* q, 
  * ckv_score_select, whose cache descriptor then needs shapes only: k = v =
  * NULL, the graph's T_cap) are read through the block table.  out, nbr8 as
  * there; entries outside [0, len[b]) or in a bad block are skipped (and are no
- * neighbours).  One launch, two when nbr8 or k_new is not NULL.
+ * neighbours), with CKV_DEVERR_BLOCK but for the sinks that a request shorter than
+ * S does not hold.  One launch, two when nbr8 or k_new is not NULL.
  * k_new [B, Hkv, d] (cache dtype, contiguous) not NULL: the new token, which
  * will be position len[b] of request b, also joins a community of every
  * graph unit as in ckv_sparse_decode_append (same rule and results; assigned

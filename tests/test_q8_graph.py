@@ -1,6 +1,7 @@
 """Community graphs over the paged 8-bit cache when its requests do not all start alike and simply grow: growth refused
-after a token has joined, idle requests, tokens given back, requests that end, requests of different length and new ones.  A join that is undone leaves no trace, which is compared bit
-for bit with the state before it; no position is ever attended twice."""
+after a token has joined, idle requests, tokens given back, requests that end, requests of different length and new ones.
+A join that is undone leaves no trace, which is compared bit for bit with the state before it; no position is ever
+attended twice."""
 import ctypes
 import re
 
@@ -9,6 +10,7 @@ import pytest
 import torch
 
 import graph_community_sparse_b200 as ckv
+import q8_ref as Q
 from graph_community_sparse_b200.layer import PagedLayerState
 from test_abi import CAPACITY, FAKE, HEADER, INVALID, WORKSPACE, _graph
 from test_q8_abi import _q8, _table
@@ -519,3 +521,34 @@ def test_build_flags_what_it_cannot_use():
     c.len[1] = 160 * 16 + 1
     st.build(labels.to(DEV), requests=i32([1, 0, 0]))  # requests left out are not looked at
     assert ckv.ckv_get_device_error(c) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", ["group", "head"])
+def test_empty_and_short_requests_decode_beside_long_ones(mode):
+    """Rows without a request, and requests shorter than the sinks: their lists name sinks that are not there, which is no
+    fault.  Outputs are those of the dense call, which every request's list covers."""
+    lens = [0, 3, 300, 1, 4, 0, 17]
+    st, labels = ragged(lens, mode)
+    st.build(labels.to(DEV))
+    c, G = st.cache, st.graph.U // len(lens)
+    q, k = torch.randn((7, 4, 64), device=DEV), torch.randn((7, 2, 64), device=DEV)
+    live = i32([1 if n else 0 for n in lens])
+    for step in range(3):
+        st.select(q, 10 ** 6)
+        sparse = st.attend(q, k).clone()
+        dense = st.dense(q, torch.empty_like(sparse))
+        assert not sparse[0].any() and not sparse[5].any()
+        K, V = st.read(300)
+        S = torch.einsum("bhd,bhtd->bht", q.abs(), K.abs().repeat_interleave(2, 1)).max() / 8
+        assert (sparse - dense).abs().max() <= 2 * Q.attention_tol(float(S), 300, float(V.abs().max()))  # one bound each
+        asg = st.assigned.view(7, G)
+        assert (asg[[0, 1, 3, 5]] == -1).all() and (asg[[2, 6]] >= 0).all()  # nobody to join, in the short ones
+        st.grow(live, 7)
+        st.write(*[torch.zeros((7, 2, 64), device=DEV)] * 2)
+        st.grow(-live, 0)  # (tokens that joined nobody are read by the dense call alone)
+        assert c.len.tolist() == lens
+        assert ckv.ckv_get_device_error(c, reset=True) == 0 and ckv.ckv_get_device_error(st.graph) == 0
+    c.len[1] = -1  # a bad length is one
+    st.attend(q)
+    assert ckv.ckv_get_device_error(c) == ckv.DEVERR_BLOCK
