@@ -399,12 +399,16 @@ def ckv_kernel_times() -> dict:
 
 def ckv_get_device_error(graph, reset: bool = False, stream=None) -> int:
     """The device error word (OR of DEVERR_* bits) of a Graph, a BlockTable or
-    a Q8Cache once the stream's queued work is done; reset=True zeroes it
-    afterwards."""
+    a Q8Cache once the queued work of the stream (by default the current one of
+    the word's device) is done; reset=True zeroes it afterwards."""
     code = ctypes.c_int32(0)
+    dev = graph.dev_err.device
+    if dev.type != "cuda":
+        raise ValueError(f"ckv_get_device_error: the error word must be on a CUDA device, not {dev}")
     desc = graph.desc if isinstance(graph.desc, GraphDesc) else GraphDesc(dev_err=graph.dev_err.data_ptr())
-    _check(lib.ckv_get_device_error(ctypes.byref(desc), _stream(stream), ctypes.byref(code), int(reset)),
-           "ckv_get_device_error")
+    with torch.cuda.device(dev):
+        _check(lib.ckv_get_device_error(ctypes.byref(desc), _stream(stream), ctypes.byref(code), int(reset)),
+               "ckv_get_device_error")
     return int(code.value)
 
 

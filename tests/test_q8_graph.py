@@ -85,6 +85,47 @@ def test_build_binding_refuses(bad):
         bad(c, g, torch.zeros((4, 8), dtype=torch.int32), torch.zeros(1 << 16, dtype=torch.uint8))
 
 
+def test_the_error_word_is_read_on_its_own_device(monkeypatch):
+    """With that device current, on its current stream; never through a host pointer."""
+    cache = ckv.new_q8_cache(2, 2, 4, 64, 8, 16, 4, device="cpu")
+    with pytest.raises(ValueError):
+        ckv.ckv_get_device_error(cache)
+    with pytest.raises(ValueError):
+        ckv.ckv_get_device_error(ckv.new_graph(ckv.q8_shape(cache, 64), ckv.PER_GROUP, 0, 4, 4, device="cpu"))
+    at = []
+
+    class Word:
+        device = torch.device("cuda", 3)
+
+        def data_ptr(self):
+            return FAKE
+
+    class Table:
+        desc, dev_err = ckv.TableDesc(), Word()
+
+    class Device:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            at.append(self.d)
+
+        def __exit__(self, *a):
+            at.append(None)
+
+    class Lib:
+        @staticmethod
+        def ckv_get_device_error(desc, stream, code, reset):
+            at.append(stream)
+            return 0
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(ckv, "_stream", lambda s: ("stream of", at[-1], s))
+    monkeypatch.setattr(ckv, "lib", Lib)
+    assert ckv.ckv_get_device_error(Table()) == 0
+    assert at == [torch.device("cuda", 3), ("stream of", torch.device("cuda", 3), None), None]
+
+
 def test_trim_null_descriptors():
     assert ckv.lib.ckv_trim_graph_q8(None, R(_graph()), None) == INVALID
     assert ckv.lib.ckv_trim_graph_q8(R(_q8(_table())), None, None) == INVALID
