@@ -587,6 +587,10 @@ ckv_status ckv_q8_workspace_size(const ckv_q8_desc* cache, const ckv_graph_desc*
     if (!bytes) return fail(CKV_ERR_INVALID_ARG, "bytes is NULL");
     CKV_TRY(check_q8(cache));
     if (graph) CKV_TRY(check_q8_graph(cache, graph));
+    if (graph && sel) {
+        const ckv_cache_desc shape = q8_shape(cache, graph->T_cap);
+        CKV_TRY(check_sel(graph, sel, (int64_t)shape.B * graphs_per_seq(&shape, graph)));
+    }
     *bytes = q8_ws_bytes(cache, graph, sel ? sel->tok_cap : graph ? graph->T_cap : 0);
     return ok();
 }

@@ -12,7 +12,7 @@ import torch
 import graph_community_sparse_b200 as ckv
 import q8_ref as Q
 from graph_community_sparse_b200.layer import PagedLayerState
-from test_abi import CAPACITY, FAKE, HEADER, INVALID, WORKSPACE, _graph
+from test_abi import CAPACITY, FAKE, HEADER, INVALID, WORKSPACE, _graph, _sel
 from test_q8_abi import _q8, _table
 
 DEV = "cuda"
@@ -83,6 +83,15 @@ def test_build_binding_refuses(bad):
     g = ckv.new_graph(ckv.q8_shape(c, 64), ckv.PER_GROUP, 0, 4, 4, device="cpu")
     with pytest.raises(ValueError):
         bad(c, g, torch.zeros((4, 8), dtype=torch.int32), torch.zeros(1 << 16, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("kw", [dict(tok_cap=0), dict(tok_cap=-5), dict(tok_cap=3), dict(tok_cap=1 << 30), dict(n_tok=None)])
+def test_workspace_of_a_bad_selection_is_refused(kw):
+    """A size for what no call would take (a negative capacity wrapped around) is not given out."""
+    out = ctypes.c_size_t(77)
+    st = ckv.lib.ckv_q8_workspace_size(R(_q8()), R(_graph()), R(_sel(**kw)), R(out))
+    assert st == (3 if kw.get("tok_cap") == 1 << 30 else INVALID) and out.value == 77
+    assert ckv.lib.ckv_q8_workspace_size(R(_q8()), None, R(_sel(**kw)), R(out)) == 0  # the dense call's alone
 
 
 def test_the_error_word_is_read_on_its_own_device(monkeypatch):
