@@ -602,3 +602,35 @@ def test_empty_and_short_requests_decode_beside_long_ones(mode):
     c.len[1] = -1  # a bad length is one
     st.attend(q)
     assert ckv.ckv_get_device_error(c) == ckv.DEVERR_BLOCK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("padded", [False, True])
+def test_rows_of_refused_requests_leave_the_pool(fmt, padded):
+    """Of three requests that grow in one call two are refused, for want of blocks and of table; their rows change no code
+    and no scale, and the third's only its own slots'."""
+    c = ckv.new_q8_cache(4, 2, 2, 64, 12, 16, 5, fmt, torch.float32)
+    p = ckv.new_plan(c, 200)
+    ckv.ckv_plan_blocks(c, i32([40, 10, 30, 70]), p)
+    gen = torch.Generator().manual_seed(2)
+    rows = torch.randn((2, 200, 2, 64), generator=gen).to(DEV)
+    ckv.ckv_quant_append(c, p, rows[0], rows[1])
+    assert p.granted.tolist() == [40, 10, 30, 70]
+    before = [x.clone() for x in (c.k.view(torch.uint8), c.v.view(torch.uint8), c.k_scale, c.v_scale)]
+    add = [30, 5, 50, 20]  # one block is free: 0 wants two; 1 grows inside its block; 2 wants three; 3 passes the table
+    ckv.ckv_plan_blocks(c, i32(add), p)
+    assert p.granted.tolist() == [0, 5, 0, 0] and ckv.ckv_get_device_error(c, reset=True) == ckv.DEVERR_PLAN
+    big = 100 * torch.randn((2, 200, 2, 64), generator=gen).to(DEV)
+    if padded:
+        ckv.ckv_quant_append(c, p, *(x.view(4, 50, 2, 64) for x in big))
+    else:
+        ckv.ckv_quant_append(c, p, big[0], big[1])
+    block = int(c.table[1, 0])
+    for now, old in zip((c.k.view(torch.uint8), c.v.view(torch.uint8), c.k_scale, c.v_scale), before):
+        others = [x for x in range(12) if x != block]
+        assert torch.equal(now[others], old[others])
+        assert not torch.equal(now[block], old[block])
+        if now.dim() == 4:
+            assert torch.equal(now[block, :, 15:], old[block, :, 15:])  # rows behind the last token
+    assert ckv.ckv_get_device_error(c) == 0

@@ -186,6 +186,157 @@ def test_v_scales_that_fall_or_rise_where_the_scores_jump(fmt, d, gq, v_scales):
 
 
 # ---------------------------------------------------------------------------
+# the size of the rounding errors
+# ---------------------------------------------------------------------------
+
+def rms_tol(S):
+    """Bound of the outputs' error relative to their size, both as root mean squares, for V of mean zero that knows
+    nothing of the errors: an error of at most e in each weight moves an output by e sqrt(sum w^2) sigma, which is e
+    times the output's own size.  e: the score's share, exp2 and the two fp16 terms of a weight 2^-22 each, and 2^-20 for
+    the scale products and the sums in fp32 (a few dozen additions, each 2^-24 of a partial sum).  The weights' sum has
+    at most the same error, apart from it: sqrt(2)."""
+    return math.sqrt(2) * (score_share(S) + 2 * 2.0 ** -22 + 2.0 ** -20)
+
+
+def relative_rms(got, want):
+    return float(((got - want) ** 2).mean() ** 0.5 / (want ** 2).mean() ** 0.5)
+
+
+def in_two(x, terms):
+    """x as a sum of fp16 terms."""
+    hi = x.astype(np.float16).astype(np.float64)
+    return hi if terms == 1 else hi + (x - hi).astype(np.float16).astype(np.float64)
+
+
+@pytest.mark.parametrize("n", [33, 1000])
+@pytest.mark.parametrize("q_terms,w_terms", [(2, 2), (1, 2), (2, 1)])
+def test_the_bound_sees_a_lost_term(n, q_terms, w_terms):
+    """The kernel's fp16 splits of q and of the weights modelled in float64: the bound holds with both terms and fails
+    where either lo term is dropped, which the wider bounds of the other tests would let pass."""
+    rng = np.random.default_rng(n)
+    d, H = 128, 64
+    k, v = rng.integers(-127, 128, (2, n, d)) / 73.0
+    q = (0.1 * rng.standard_normal((H, d))).astype(np.float32).astype(np.float64)
+    top = np.exp2(np.floor(np.log2(np.abs(q).max(1, keepdims=True))) - 14)
+    got, want, S = [], [], 0.0
+    for h in range(H):
+        o, s = Q.attention(q[h], k, v)
+        w = np.exp(k @ (in_two(q[h] / top[h], q_terms) * top[h]) / math.sqrt(d))
+        w = in_two(w * 32 / w.max(), w_terms)
+        got.append(w @ v / w.sum())
+        want.append(o)
+        S = max(S, s)
+    err = relative_rms(np.array(got), np.array(want))
+    assert (err <= rms_tol(S)) == (q_terms == w_terms == 2), (err, rms_tol(S))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,gq", [(64, 8), (128, 4), (128, 8), (64, 2)])
+@pytest.mark.parametrize("n", [33, 200, 1000, 5000, 70000])
+def test_rounding_errors_keep_their_size(fmt, dtype, d, gq, n):
+    Hkv = 2
+    cache = pool([n], Hkv, gq, d, 64, fmt, dtype)
+    gen = torch.Generator(device=DEV).manual_seed(n + d + gq)
+    for t, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        x = torch.randint(-127, 128, t.shape, generator=gen, device=DEV, dtype=torch.int32).to(torch.float32)
+        t.copy_(x.to(t.dtype))
+        s.copy_((1 + torch.rand(s.shape, generator=gen, device=DEV)) / 100)
+    q = (0.1 * torch.randn((1, Hkv * gq, d), generator=gen, device=DEV)).to(dtype)
+    outs, _, _ = every_way(cache, q)
+    ids = cache.table[0].long()
+    K, V = ((t[ids].float().double() * s[ids].double()[:, :, None, None]).transpose(0, 1).reshape(Hkv, -1, d)[:, :n]
+            for t, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+    qd = q[0].double().view(Hkv, gq, d)
+    want = torch.softmax(torch.einsum("hgd,htd->hgt", qd, K) / math.sqrt(d), -1) @ V
+    S = float((torch.einsum("hgd,htd->hgt", qd.abs(), K.abs()) / math.sqrt(d)).max())
+    for out in outs:
+        err = relative_rms(out[0].double().view(Hkv, gq, d), want)
+        assert err <= rms_tol(S), (err, rms_tol(S))
+
+
+# ---------------------------------------------------------------------------
+# long lists
+# ---------------------------------------------------------------------------
+
+def check_permuted(cache, q, S_sinks, neighbours):
+    """Lists of all of a request's tokens in random order, a list a KV head, against the dense reference in float64; the
+    neighbours' logits against the eight largest."""
+    lens = cache.len.tolist()
+    B, Hkv, Hq, d = cache.B, cache.Hkv, cache.Hq, cache.d
+    cap, gq = max(lens), Hq // Hkv
+    shape = ckv.q8_shape(cache, cap)
+    graph = ckv.new_graph(shape, ckv.PER_GROUP, S_sinks, 1, 0)
+    sel = ckv.new_selection(shape, graph, cap)
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    for u in range(graph.U):
+        n = lens[u // Hkv]
+        sel.sel_tok[u, :n] = torch.randperm(n, generator=gen, device=DEV).to(torch.int32)
+    sel.n_tok.copy_(i32([lens[u // Hkv] for u in range(graph.U)]))
+    out = torch.full(q.shape, float("nan"), device=DEV)
+    nbr = torch.full((graph.U, 8), -7, dtype=torch.int32, device=DEV) if neighbours else None
+    ws = ckv.new_workspace(ckv.ckv_q8_workspace_size(cache, graph, sel))
+    for _ in range(2):
+        ckv.ckv_sparse_decode_q8(cache, q, graph, sel, out, nbr, ws)
+    assert not ws[256: 256 + 8192 * 4].any()  # the counters are zero again
+    for b, n in enumerate(lens):
+        if n == 0:
+            assert not out[b].any()
+            continue
+        ids = cache.table[b, : -(-n // cache.desc.blocks.block)].long()
+        K, V = ((t[ids].float().double() * s[ids].double()[:, :, None, None]).transpose(0, 1).reshape(Hkv, -1, d)[:, :n]
+                for t, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+        qd = q[b].double().view(Hkv, gq, d)
+        x = torch.einsum("hgd,htd->hgt", qd, K) / math.sqrt(d)
+        S = float((torch.einsum("hgd,htd->hgt", qd.abs(), K.abs()) / math.sqrt(d)).max())
+        tol = Q.attention_tol(S, n, float(V.abs().max()))
+        assert float((out[b].double().view(Hkv, gq, d) - torch.softmax(x, -1) @ V).abs().max()) <= tol
+        for h in range(Hkv if neighbours else 0):
+            u, best = b * Hkv + h, x[h].amax(0)
+            skipped = sel.sel_tok[u, : min(S_sinks, n)].long()  # the list's first entries take the sinks' places
+            best[skipped] = -math.inf
+            m = min(8, n - len(skipped))
+            got = nbr[u].tolist()
+            assert len(set(got[:m])) == m and got[m:] == [-1] * (8 - m)
+            if m:
+                cut = float(best.topk(m).values[-1])
+                assert float(best[torch.tensor(got[:m], device=DEV)].min()) >= cut - 2 * score_share(S)
+
+
+def random_pool(lens, Hkv, gq, d, block, fmt, dtype, seed):
+    cache = pool(lens, Hkv, gq, d, block, fmt, dtype, seed)
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    for t, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        x = torch.randint(-127, 128, t.shape, generator=gen, device=DEV, dtype=torch.int32).to(torch.float32)
+        t.copy_(x.to(t.dtype))
+        s.copy_((1 + torch.rand(s.shape, generator=gen, device=DEV)) / 100)
+    return cache, torch.randn((len(lens), Hkv * gq, d), generator=gen, device=DEV).to(dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("neighbours", [False, True])
+@pytest.mark.parametrize("lens", [[1023, 1024, 1025, 192, 193], [4095, 4097, 4096], [32767, 16], [32768], [32769, 50000]])
+def test_lists_where_the_least_piece_changes(lens, neighbours):
+    """Lists of 12, 64, 256 and 2048 tiles and their neighbours."""
+    cache, q = random_pool(lens, 1, 4, 64, 64, "int8", torch.float32, len(lens))
+    check_permuted(cache, q, 0, neighbours)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("neighbours", [False, True])
+@pytest.mark.parametrize("gq,d,fmt", [(1, 64, "int8"), (8, 64, "e4m3"), (4, 128, "int8")])
+def test_lists_laid_end_to_end(gq, d, fmt, neighbours):
+    """More lists than blocks of the grid, a few so long that many blocks share them, some empty."""
+    lens = [100 + b % 37 for b in range(330)]
+    lens[3], lens[100], lens[101], lens[329] = 30000, 9000, 20001, 25000
+    for b in range(5, 330, 11):
+        lens[b] = 0
+    cache, q = random_pool(lens, 2, gq, d, 32, fmt, torch.bfloat16, gq)
+    check_permuted(cache, q, 2, neighbours)
+
+
+# ---------------------------------------------------------------------------
 # sizes of the read, without a GPU
 # ---------------------------------------------------------------------------
 
