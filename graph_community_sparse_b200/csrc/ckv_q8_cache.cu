@@ -169,6 +169,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
             t.free_list[avail - 1 - (k0 + i)] = id[i];
             t.table[at[i]] = -1;
         }
+        const unsigned top = max(max((unsigned)id[0], (unsigned)id[1]), max((unsigned)id[2], (unsigned)id[3]));
+        if (top >= (unsigned)t.n_blocks) atomicOr(t.dev_err, CKV_DEVERR_BLOCK);
     }
     // everybody has read len, add and n_free and given blocks back
     if (gridDim.x > 1) cluster_sync();
@@ -176,7 +178,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
 
     // blocks taken: the k-th is free_list[avail - 1 - k].  A refused request's
     // range of k is empty or belongs to nobody (all needs after the first
-    // refusal for want of blocks are refused).
+    // refusal for want of blocks are refused).  An id out of range is flagged
+    // with the slots of its rows.
     const int taken = s_need[B];
     for (int k0 = gtid * 4; k0 < taken; k0 += gthreads * 4) {
         int b = last_le(s_need, B + 1, k0);

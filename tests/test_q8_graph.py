@@ -634,3 +634,32 @@ def test_rows_of_refused_requests_leave_the_pool(fmt, padded):
         if now.dim() == 4:
             assert torch.equal(now[block, :, 15:], old[block, :, 15:])  # rows behind the last token
     assert ckv.ckv_get_device_error(c) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [-1, 40, 2 ** 31 - 1])
+def test_plan_flags_blocks_out_of_range(bad):
+    """A block id that is none, in the table of a request that gives it back or in the free list, is flagged by the plan
+    that meets it, rows or not; an id that is not met is not looked at."""
+    for rows in (0, 5000):
+        c = ckv.new_q8_cache(3, 1, 1, 64, 40, 16, 12)
+        p = ckv.new_plan(c, 200)
+        ckv.ckv_plan_blocks(c, i32([33, 64, 100]), p)
+        assert ckv.ckv_get_device_error(c) == 0
+        c.table[0, 2] = bad
+        c.blocks.free_list[0] = bad
+        p = ckv.new_plan(c, rows)
+        ckv.ckv_plan_blocks(c, i32([0, -64, 0]), p)
+        assert ckv.ckv_get_device_error(c) == 0
+        ckv.ckv_plan_blocks(c, i32([-1, 0, 0]), p)
+        assert ckv.ckv_get_device_error(c, reset=True) == ckv.DEVERR_BLOCK
+        assert c.len.tolist() == [32, 0, 100]
+    # taken from the free list: the 30th block from its top, by a request of its own
+    c = ckv.new_q8_cache(2, 1, 1, 64, 40, 16, 40)
+    c.blocks.free_list[39 - 30] = bad
+    p = ckv.new_plan(c, 640)
+    ckv.ckv_plan_blocks(c, i32([30 * 16, 0]), p)
+    assert ckv.ckv_get_device_error(c) == 0
+    ckv.ckv_plan_blocks(c, i32([0, 16]), p)
+    assert ckv.ckv_get_device_error(c) == ckv.DEVERR_BLOCK
+    assert p.slot.tolist()[:16] == [-1] * 16
