@@ -16,10 +16,9 @@
 // B, so 16 tokens cost 2 d/16 products:
 //   S [token, head]  = K [token, dim]  Q^T [dim, head]
 //   O [dim, head]   += V^T [dim, token] P [token, head]
-// d = 128, 4 heads: 331 warp instructions for 16 tokens of int8 (195 of them on the
-// integer pipe), 265 of e4m3; 445 with a conversion by shifts and tiles of 16 tokens.
-// At the copy rate that is about half of the issue slots (the captures: 46 % and
-// 37 %), the tensor pipe 17 %.
+// d = 128, 4 heads, all of a call's instructions counted: 380 warp instructions for 16
+// tokens of int8, 277 of e4m3.  That is about half of the issue slots (the captures:
+// 49 % and 37 %), the tensor pipe 17 %.
 // A q row is normalised to a power of two and held as fp16 hi + lo (22 bits),
 // and so is a weight; with at most 4 heads a group hi and lo are columns 0..3
 // and 4..7 of one product, with 8 heads they take a product each.

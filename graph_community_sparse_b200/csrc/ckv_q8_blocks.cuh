@@ -10,8 +10,9 @@
 // the units are laid end to end and cut into equal ranges, which may cross units.
 // The second way costs a block that crosses a unit about 12 tiles' time (a new
 // query, an empty ring, a join), the first the difference between the longest
-// piece and the share: the smaller loss decides (33 ragged requests 38.7 us, by ranges
-// 48.6; 8 requests of 128K tokens, whose pieces do not fit, 342, by pieces 355).
+// piece and the share: the smaller loss decides (33 ragged requests 40.6 us, by ranges
+// 50.6, one of 32K tokens 23.5 and 26.5; 8 requests of 128K tokens, whose pieces do not
+// fit, 341, by pieces 355 with 342 beside it).
 // (Finer pieces by ticket, for the SMs' 10 % difference in bandwidth, lost more by
 // their starts: 8 requests of 128K tokens 357 against 350 us, 8 heads a group at 64K
 // 249 against 200.)
@@ -27,13 +28,13 @@
 // entries ahead of the copies, and each row brings its own two scales.
 //
 // What bounds it: all tokens, HBM: 8 requests of 128K tokens, 8 heads of 128, in
-// int8 336 to 354 us for 2.15 GB, 0.97 to 0.93 of the copy rate; 4 requests in e4m3
-// 177 us, 0.93; d = 64 0.84; 8 query heads a KV head 0.92.  Short work has about 13 us
+// int8 332 to 367 us for 2.15 GB, 0.98 to 0.89 of the copy rate; 4 requests in e4m3
+// 178 us, 0.92; d = 64 0.83; 8 query heads a KV head 0.90.  Short work has about 13 us
 // on top of its bytes: the launch, the chain length - block - rows, the join (1
-// request of 32K tokens 24 us, 33 ragged ones up to 9000 tokens 38 us).  Lists: 256 of
+// request of 32K tokens 24 us, 33 ragged ones up to 9000 tokens 40 us).  Lists: 256 of
 // 2052 tokens of 128K, one a query head: 50 us.  Their rows are scattered 128 bytes,
 // of which HBM gives 4.4 to 4.7 TB/s (29 us for these); the rest is the start, the
-// join and two scale loads a row.  8 lists of 2052 tokens: 11.5 us, of 8000: 17.5, one
+// join and two scale loads a row.  8 lists of 2052 tokens: 11.5 us, of 8000: 17.2, one
 // of 132: 7 us.
 #pragma once
 
@@ -59,7 +60,7 @@ __device__ __forceinline__ int least_piece(int nt) {
 }
 
 // Rows in order: tiles of two halves, 12 warps an SM (64K tokens with 8 heads a group
-// 181 us, d = 64 99 us; one half, 16 warps: 200 and 118).  Lists, which wait longer for
+// 182 us, d = 64 99 us; one half, 16 warps: 200 and 118).  Lists, which wait longer for
 // scattered rows: one half, 16 warps (256 lists of 128K tokens 53 us; two halves 59).
 template <int D, bool LIST>
 struct QdShape {
@@ -607,7 +608,7 @@ static cudaError_t launch_blocks_q8_q(const BlocksQ8Params& p, long long most, c
 
 template <int D, int GQ, int FMT, bool LIST, bool NBR = false>
 static cudaError_t launch_blocks_q8_t(const BlocksQ8Params& p, long long most, cudaStream_t st) {
-    if constexpr (GQ == 8) {
+    if constexpr (GQ == 8) {  // 33 ragged requests 40 us, with lo parts 44; 8 of 64K tokens 182, with them 189
         if (p.c.dtype == CKV_DTYPE_BF16) return launch_blocks_q8_q<D, GQ, FMT, LIST, NBR, false>(p, most, st);
     }
     return launch_blocks_q8_q<D, GQ, FMT, LIST, NBR, true>(p, most, st);

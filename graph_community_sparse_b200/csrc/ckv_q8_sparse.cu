@@ -6,8 +6,9 @@
 // block-split kernel (ckv_q8_blocks.cuh) attends; when neighbours are wanted it also
 // stores each entry's graph logit, and a small kernel launched as its programmatic
 // dependent searches them and runs the fused update, a block per graph unit (the
-// search of ckv_decode.cuh): a chain of dependent loads, 4 to 8 us after the attention
-// (8 lists of 2052 tokens 11.5 -> 15.5 us, 256 of them 50 -> 59 us).
+// search of ckv_decode.cuh): a chain of dependent loads, 4 to 9 us after the attention
+// (8 lists of 2052 tokens 11.5 -> 15.8 us, 256 of them 51 -> 60 us), and the update 3 to
+// 5 us more.
 #include "ckv_q8_blocks.cuh"
 
 namespace ckv {

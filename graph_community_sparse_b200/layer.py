@@ -144,6 +144,7 @@ class PagedLayerState:
     Joins are undone by the grow() that refuses their token, adds none, or gives
     it back later; a request that falls below the positions its communities were
     built over loses them (DEVERR_CUT, unless it ended) until the next build().
+    What undoing takes is kept for the tail: max_tail centres (fp32) a graph unit.
     grow()'s plan buffers are used again by the next grow() of as many rows; those
     of more than KEEP_ROWS rows only live until a grow() of another number.
     """
