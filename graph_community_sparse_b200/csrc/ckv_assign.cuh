@@ -154,9 +154,9 @@ __device__ __forceinline__ void write_scoring_copy(const AssignParams& p, size_t
 // candidates w, w + NW, ... with all of their centres requested before any
 // is used; warp 0 picks the winner and moves its centre.  APPEND: the last
 // warp also writes the new K/V rows (append_rows; the attention's merge
-// kernel does that itself, off the update's path).  UNDO: the winner's centre
-// as it was is kept in p.undo, where there is one.
-template <typename T, int D, int NW, bool APPEND, bool UNDO = false, typename Sync>
+// kernel does that itself, off the update's path).  The winner's centre as it
+// was is kept in p.undo, where there is one.
+template <typename T, int D, int NW, bool APPEND, typename Sync>
 __device__ __forceinline__ void assign_unit(const AssignParams& p, int u, const int* nbrpos, int tid,
                                             AssignScratch<D>& sc, Sync sync) {
     constexpr int E = D / 32;
@@ -282,12 +282,10 @@ __device__ __forceinline__ void assign_unit(const AssignParams& p, int u, const 
     const float* c0r = sc.row[bi] + lane * E;
     const float inv_n1 = __frcp_rn((float)(n + 1));  // one reciprocal, then products
     float c1[E], amax = 0.f;
-    if constexpr (UNDO) {
-        if (p.undo) {
-            float* un = p.undo + ((size_t)u * p.max_tail + tl) * D + lane * E;
+    if (p.undo) {
+        float* un = p.undo + ((size_t)u * p.max_tail + tl) * D + lane * E;
 #pragma unroll
-            for (int e = 0; e < E; ++e) un[e] = c0r[e];
-        }
+        for (int e = 0; e < E; ++e) un[e] = c0r[e];
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) {

@@ -148,7 +148,7 @@ __device__ __forceinline__ void merge_assign(const DecodeParams& p, int u, const
             if (xt < 32) untail_unit<D>(ap, u, ap.pos, xt);
             sync();
         }
-        assign_unit<T, D, NBR_WARPS, false, true>(ap, u, nbpos, xt, s_as, sync);
+        assign_unit<T, D, NBR_WARPS, false>(ap, u, nbpos, xt, s_as, sync);
     } else {
         assign_unit<T, D, NBR_WARPS, false>(p.ap, u, nbpos, xt, s_as, sync);
     }

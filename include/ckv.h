@@ -149,12 +149,12 @@ typedef struct {
  *   tail_len int32 [U]
  *   dev_err  int32 [1]          OR of CKV_DEVERR_* bits; the caller zeroes it
  *   undo     fp32  [U, max_tail, d] or NULL: the centre of its community before
- *                  each tail member joined, kept by ckv_sparse_decode_q8 so that
- *                  the member can be taken out again
+ *                  each tail member joined, kept by every call that joins one
+ *                  so that the member can be taken out again
  *   built    int32 [U] or NULL  positions [0, built) were labelled when the unit
  *                  was built (0: never); written by the builds
  * undo and built are for the graphs of a paged 8-bit cache, whose requests can
- * lose tokens (ckv_trim_graph_q8); the other calls leave undo alone.
+ * lose tokens (ckv_trim_graph_q8).
  * assign_rule is a ckv_assign_rule; any other value is CKV_ERR_INVALID_ARG.
  * S sink positions 0..S-1 belong to no community and are always attended
  * ([R-A] paragraph 3).  T_cap here must equal the cache's T_cap.
@@ -592,7 +592,8 @@ CKV_API ckv_status ckv_build_centroids_q8(const ckv_q8_desc* cache, const int32_
  * Brings a graph in step with the lengths that ckv_plan_blocks left: call it
  * after a ckv_plan_blocks that may refuse a joined token or drop tokens, before the
  * next ckv_score_select.  In every graph unit of request b the tail members at
- * positions >= len[b] leave, last first; counts, comm_of, centres and their scoring
+ * positions >= len[b] leave, last first (members joined in ascending order of
+ * position, as ckv_sparse_decode_q8 joins them, are the tail's end); counts, comm_of, centres and their scoring
  * copies are then, bit for bit, what they were before those members joined.  A
  * unit built over more than len[b] positions is emptied (no community, no member;
  * its selection is the sinks alone until it is built again), with CKV_DEVERR_CUT

@@ -663,3 +663,36 @@ def test_plan_flags_blocks_out_of_range(bad):
     ckv.ckv_plan_blocks(c, i32([0, 16]), p)
     assert ckv.ckv_get_device_error(c) == ckv.DEVERR_BLOCK
     assert p.slot.tolist()[:16] == [-1] * 16
+
+
+@pytest.mark.gpu
+def test_joins_by_the_wide_calls_are_undone_too():
+    """ckv_assign_update, ckv_append_assign and ckv_sparse_decode_append on the paged graph (rows read back into a wide
+    cache): what they join, the trim takes out."""
+    b = Batch(T=90)
+    st, c = b.st, b.cache
+    K, V = (torch.zeros((3, 2, 160, 64), device=DEV) for _ in range(2))
+    k, v = st.read(90)
+    K[:, :, :90], V[:, :, :90] = k, v
+    wide = ckv.cache_desc(K, V, 4)
+    ws = ckv.new_workspace(ckv.ckv_workspace_size(wide, st.graph, st.sel))
+    before = b.state()
+    states = []
+    for pos, how in ((90, "fused"), (91, "append"), (92, "update")):
+        q, (kn, vn) = b.q(), b.rows()
+        st.select(q, 10 ** 6)
+        ckv.ckv_sparse_decode(wide, q, st.graph, st.sel, st.out, st.nbr8, ws)
+        if how == "fused":
+            ckv.ckv_sparse_decode_append(wide, q, st.graph, st.sel, st.out, st.nbr8, pos, kn, vn, st.assigned, ws)
+        elif how == "append":
+            ckv.ckv_append_assign(wide, st.graph, pos, kn, vn, st.nbr8, st.assigned)
+        else:
+            K[:, :, pos], V[:, :, pos] = kn, vn
+            ckv.ckv_assign_update(wide, st.graph, pos, st.nbr8, st.assigned)
+        states.append(b.state())
+        assert (st.assigned >= 0).all() and st.graph.tail_len.tolist() == [pos - 89] * 6
+    c.len.copy_(i32([92, 91, 90]))
+    ckv.ckv_trim_graph_q8(c, st.graph)
+    after = b.state()
+    for r, want in enumerate((states[1], states[0], before)):
+        same(want, after, range(2 * r, 2 * r + 2))
