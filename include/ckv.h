@@ -482,8 +482,8 @@ typedef struct {
  * then position) is free_list[n_free - 1 - k], and a drop puts its blocks back
  * so that a growth of the same requests takes the same blocks again.  Entries
  * of free_list past the new n_free keep what they held.
- * table, len, free_list and n_free are updated in place.  One launch, two for
- * more than 4096 rows.
+ * table, len, free_list and n_free are updated in place (community graphs follow
+ * by ckv_trim_graph_q8).  One launch, two for more than 4096 rows.
  */
 CKV_API ckv_status ckv_plan_blocks(const ckv_table_desc* blocks, const int32_t* add, const ckv_plan_desc* plan,
                                    ckv_stream_t stream);
